@@ -153,6 +153,8 @@ int log2_up(int64_t n) {
 hipError_t launch_w4(const cbs_w4_desc &d, const cbs_w4_args &a, hipStream_t stream) {
   const int x = d.dtype == CBS_I8 ? 0 : d.dtype == CBS_F16 ? 1 : d.dtype == CBS_BF16 ? 2 : 3;
   const int size = kW4Bytes[x];
+  // A group that is longer than k is one group all the same: cut to k's blocks, no sum or product of it leaves 31 bits.
+  const int group = std::min(d.group, std::max(kW4Block, (d.k + kW4Block - 1) / kW4Block * kW4Block));
   W4Params p = {};
   p.ring = x != 3 && d.k >= kW4Block && (uintptr_t)a.x % 16 == 0 && a.x_stride * size % 16 == 0;
   // Blocks of 16 rows of a workgroup: as many as there are, where its output tiles then fill the card; fewer where not, for more
@@ -162,11 +164,11 @@ hipError_t launch_w4(const cbs_w4_desc &d, const cbs_w4_args &a, hipStream_t str
   const int most_rb = tiles16 <= (x == 3 ? 2048 : 256) ? 1 : tiles16 <= 1024 || x == 3 ? 2 : 4;
   const int rb = std::min(most_rb, a.rows <= 16 ? 1 : a.rows <= 32 ? 2 : 4), stage = rb * 16 * kW4Block * size;
   p.a = a;
-  p.k = d.k, p.n = d.n, p.group = d.group, p.out_dtype = d.out_dtype, p.scale_dtype = d.scale_dtype;
+  p.k = d.k, p.n = d.n, p.group = group, p.out_dtype = d.out_dtype, p.scale_dtype = d.scale_dtype;
   p.code_stride = (d.k + 31) / 32 * 16;
   p.blocks = (d.k + kW4Block - 1) / kW4Block;
-  p.groups = (d.k + d.group - 1) / d.group;
-  p.by_wide = make_fastdiv(std::max(1, d.group / kW4Block));
+  p.groups = (d.k + group - 1) / group;
+  p.by_wide = make_fastdiv(std::max(1, group / kW4Block));
   p.by_whole = make_fastdiv(std::max(1, d.k / 8));
   // All of x in LDS: room for two workgroups on a compute unit, or where x cannot go there straight, one.  us with room for one
   // and without: float32 1 row 4096 -> 4096 7.2 and 15.1, 4 rows 4096 -> 11008 16.7 and 19.1; x that can, 16 rows 4096 -> 4096 of
@@ -200,7 +202,7 @@ hipError_t launch_w4(const cbs_w4_desc &d, const cbs_w4_args &a, hipStream_t str
     // 23.8; 32 rows 8192 -> 8192 2: 17.6, 1: 25.2, 4: 27.0; 64 rows 8192 -> 16384 2: 36, 1: 48; 32 rows 8192 -> 28672 4: 39.2, 2: 42.1.
     const int64_t wanted = d.n * ((a.rows + rb * 16 - 1) / (rb * 16)) / 256;
     if (p.ring) {
-      const int shared = kW4Shared[rb / 2], least = kW4Waves / shared * 16, most = rb == 4 || d.group == 32 ? 2 : 4;
+      const int shared = kW4Shared[rb / 2], least = kW4Waves / shared * 16, most = rb == 4 || group == 32 ? 2 : 4;
       while (nb < most && least * nb < wanted) nb *= 2;
       tile_n = least * nb;
       lds = std::max(2u * stage * shared, (unsigned)(4 * rb * 16 * (tile_n + 4)) * shared);
