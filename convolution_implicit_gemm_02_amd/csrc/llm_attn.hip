@@ -135,7 +135,7 @@ __device__ __forceinline__ Seq seq_of(const AttnParams &p, int b) {
 }
 // First and last key that new token i sees.
 __device__ __forceinline__ int first_key(const AttnParams &p, const Seq &s, int i) {
-  return p.window > 0 ? max(0, s.length - s.count + i - p.window + 1) : 0;
+  return p.window > 0 ? max(0, max(0, s.length - s.count + i) - p.window + 1) : 0;  // a place before the first key sees what that place does: no sum leaves 31 bits
 }
 __device__ __forceinline__ int last_key(const AttnParams &p, const Seq &s, int i) {
   return p.causal ? min(s.length - s.count + i, s.length - 1) : s.length - 1;

@@ -33,3 +33,36 @@ def test_w4_group_longer_than_k(kind, rows, k, group):
         out.append(torch.full((rows, n), math.nan, device="cuda"))
         llm.cbs_w4_linear(llm.make_w4_desc(k, n, length, dtype=KIND[kind], out_dtype=llm.CBS_F32), x, packed, scales, out[-1], zeros=zeros, x_scale=step)
     assert torch.isfinite(out[0]).all() and torch.equal(*out)
+
+
+# ---------------------------------------------------------------- attention
+
+
+def deep(made):
+    """The same with a table that has room for 2^18 tokens: enough work by its bounds that long chunks go in units of many rows."""
+    made = list(made)
+    table = torch.full((made[3].shape[0], (1 << 18) // made[4].shape[2]), -1, dtype=torch.int32)
+    table[:, : made[3].shape[1]] = made[3]
+    made[3] = table
+    return tuple(made)
+
+
+def check_made(made, heads, kv_heads, dim, kind, cache, causal=True, window=0, scale=None):
+    q, q_start, kv_len, table, k, v, ks, vs = made
+    scale = dim ** -0.5 if scale is None else scale
+    attn = llm.cbs_attn_create(llm.make_attn_desc(heads, kv_heads, dim, k.shape[2], dtype=KIND[kind], cache_dtype=KIND[cache], causal=causal, window=window, scale=scale,
+                                                  max_seqs=table.shape[0]))
+    out = base.run_attn(made, heads, kv_heads, dim, k.shape[2], kind, cache, attn=attn)
+    want, mags, tops = ref.attention(q, q_start, kv_len, table, k, v, scale, causal, window, ks, vs)
+    base.close(out, want, base.attn_bound(want, mags, tops, kind, dim, max(1, int(kv_len.max()))), "attention")
+    return out
+
+
+@pytest.mark.parametrize("kind,cache", base.PAIRS)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 5, 2**31 - 200])
+@pytest.mark.parametrize("new,kv", [([10, 6, 1], [4, 6, 0]), ([300, 150], [41, 149])])
+def test_attn_window_of_all_there_can_be(kind, cache, causal, window, new, kv):
+    """More new tokens than keys, and a window near 2^31: places before the first key, and the rows beside them, keep theirs."""
+    made = base.make_attn(new, kv, 4, 2, 64, 16, kind, cache)
+    check_made(made if len(new) == 3 else deep(made), 4, 2, 64, kind, cache, causal, window)
