@@ -800,7 +800,11 @@ __global__ __launch_bounds__(kAttnChunkThreads, 2) void attn_chunk_kernel(const 
 #pragma unroll
             for (int w = 0; w < WAVES; w++) sum |= s_wild[w];
             wild = __builtin_amdgcn_readfirstlane(sum);
-          } else {
+          }
+        }
+        if constexpr (I8) {
+          // Values' steps that are infinite or NaN: hidden ones must not meet a weight of zero, and none can be taken apart in two terms.
+          if (edge || NP > 1) {
             bool any = false;
 #pragma unroll
             for (int i = 0; i < 8; i++)

@@ -66,3 +66,36 @@ def test_attn_window_of_all_there_can_be(kind, cache, causal, window, new, kv):
     """More new tokens than keys, and a window near 2^31: places before the first key, and the rows beside them, keep theirs."""
     made = base.make_attn(new, kv, 4, 2, 64, 16, kind, cache)
     check_made(made if len(new) == 3 else deep(made), 4, 2, 64, kind, cache, causal, window)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("which", ["key", "value", "both"])
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("key", [70, 200, 300])
+@pytest.mark.parametrize("new", [1, 40, 130])
+def test_attn_nonfinite_steps_seen(bad, which, kind, key, new):
+    """A step that is infinite or NaN, in a tile that all rows see whole (70, 200) and in one that some of them see in part (300):
+    rows that do not see it stay as they are, and those that do have what the formula says of a NaN, and of an infinite step of values."""
+    heads, dim, page, kv = 4, 64, 16, 310
+    made = deep(base.make_attn([new], [kv], heads, 2, dim, page, kind, "i8", q_by=0.3))
+    q, q_start, kv_len, table, k, v, ks, vs = made
+    pg, o = int(table[0, key // page]), key % page
+    v[pg, :, ::3, o] = 0  # codes of zero, whose value is NaN
+    v[pg, :, 1::3, o] = 5
+    v[pg, :, 2::3, o] = -9
+    clean, mags, tops = ref.attention(q, q_start, kv_len, table, k, v, dim ** -0.5, True, 0, ks, vs)
+    if which != "value":
+        ks[pg, :, o] = bad
+    if which != "key":
+        vs[pg, :, o] = bad
+    out = base.run_attn(made, heads, 2, dim, page, kind, "i8").double().cpu()
+    bound = base.attn_bound(clean, mags, tops, kind, dim, kv)
+    sees = torch.arange(new) + kv - new >= key
+    if not sees.all():
+        base.close(out[~sees], clean[~sees], bound[~sees], "rows that do not see it")
+    out, want = out[sees], clean[sees].clone()
+    if which == "value":  # a weight times 0, 5 or -9 times it
+        want[..., ::3], want[..., 1::3], want[..., 2::3] = math.nan, 5 * bad, -9 * bad
+        assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(out.nan_to_num(0.0), want.nan_to_num(0.0))
+    elif math.isnan(bad):
+        assert torch.isnan(out).all()
