@@ -10,6 +10,10 @@
 // instruction gives group g the rows 4 g to 4 g + 3 of the 16 keys that it was fed; the keys are therefore fed in the order
 // that makes the scores of a group belong to GK consecutive keys, the ones whose values the group's lanes read as one
 // 16-byte piece of V^T.  No score crosses a lane; only the maximum is taken over the four lanes of a row.
+//
+// Weights that meet float16 values are float16, whose smallest is 2^-24: many keys of small weight would be lost to O and not to
+// l.  They are taken times a power of two, which O / l does not have, so that the largest is 2^15: weights down to 2^-39 of the
+// largest (long chunks, whose maximum may lag by 2^8: 2^-31) count.
 #include <type_traits>
 
 #include "llm_attn.h"
@@ -321,7 +325,7 @@ __global__ __launch_bounds__(256, QK == CBS_F32 || DS > 4 ? 1 : 2) void attn_row
 #pragma unroll
         for (int d = 0; d < DB; d++) o[d] *= keep;
       }
-      const float from = m == -INFINITY ? 0.0f : m;
+      const float from = m == -INFINITY ? 0.0f : m - (PF16 ? 15.0f : 0.0f);  // weights up to 2^15
 #pragma unroll
       for (int i = 0; i < GK; i++) {
         sc[i] = __builtin_amdgcn_exp2f(sc[i] - from);
@@ -872,7 +876,7 @@ __global__ __launch_bounds__(kAttnChunkThreads, 2) void attn_chunk_kernel(const 
         }
         float from[RB];
 #pragma unroll
-        for (int m = 0; m < RB; m++) from[m] = top[m] == -INFINITY ? 0.0f : -top[m];
+        for (int m = 0; m < RB; m++) from[m] = top[m] == -INFINITY ? 0.0f : (PF16 ? 7.0f : 0.0f) - top[m];  // weights up to 2^8, float16 2^15
 
         // pair i of the tile's weights: two keys of a row
         f32x4 sc2[RB][2];

@@ -20,7 +20,8 @@
  *   out_i = sum_j p_j v_j / sum_j p_j over the keys that it sees, p_j = exp(scale * q_i . k_j - max); 0 where it sees none.
  *   Head h reads the cache's head h / (heads / kv_heads).  What the cache holds where no key is seen, NaN and infinities
  *   among it, does not reach the output.  With 16-bit queries the weights p_j are rounded to 16 bits before they meet the
- *   values: one that float16 does not hold is zero, and an infinite value that it meets NaN.
+ *   values.  One that its type does not hold is zero (over a float16 cache below 2^-32 of the row's largest, else below that of
+ *   32 bits), and an infinite value that it meets NaN.
  *
  * Layouts (device memory; strides in elements; the innermost axis is dense):
  *   4-bit codes  uint8 [n][round_up(ceil(k / 2), 16)], input feature 2i in the low nibble of byte i, 2i + 1 in the high one;

@@ -99,3 +99,31 @@ def test_attn_nonfinite_steps_seen(bad, which, kind, key, new):
         assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(out.nan_to_num(0.0), want.nan_to_num(0.0))
     elif math.isnan(bad):
         assert torch.isnan(out).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("new,max_kv", [(1, 1), (1, None), (20, 1), (150, None), (4800, 500)])
+@pytest.mark.parametrize("drop,logn", [(26, 18), (22, 18), (29, 20)])
+def test_attn_many_small_weights(kind, new, max_kv, drop, logn):
+    """2^18 (2^20) keys of a weight that is 2^-26 (2^-22, 2^-29) of that of four keys before them, whose values are zero: all of the
+    output comes from the small ones.  Each is off by its rounding to 16 bits: half a step, which of a float16 weight of 2^-29
+    taken 2^7 times is 2^-25 of 2^-22.  max_kv: the keys in one range, or in many."""
+    heads, dim, page, many = 2, 64, 64, 1 << logn
+    q = torch.zeros(new, heads, dim, dtype=base.TYPES[kind])
+    q[..., 0] = 8.0
+    k, v = torch.zeros(2, 1, page, dim, dtype=base.TYPES[kind]), torch.ones(2, 1, dim, page, dtype=base.TYPES[kind])
+    k[1, 0, :, 0], v[1] = -100.0, 0.0
+    k[1, 0, 5, 0] = k[1, 0, 37, 0] = 4.0
+    scale = drop * math.log(2) / (8 * 4)
+    table = torch.zeros(1, 2 + many // page, dtype=torch.int32)  # one page for all of the small ones
+    table[0, :2] = 1
+    made = (q, torch.tensor([0, new], dtype=torch.int32), torch.tensor([many + 2 * page], dtype=torch.int32), table, k, v, None, None)
+    attn = llm.cbs_attn_create(llm.make_attn_desc(heads, 1, dim, page, dtype=KIND[kind], cache_dtype=KIND[kind], causal=False, scale=scale))
+    out = base.run_attn(made, heads, 1, dim, page, kind, kind, attn=attn, max_kv=max_kv)
+    one = math.exp(-8 * 4 * scale)
+    want = torch.full(out.shape, many * one / (4 + many * one), dtype=torch.float64)
+    rel, _ = base.half_step(base.TYPES[kind])
+    weight = rel if kind == "bf16" else max(rel, 2.0 ** -25 / 2.0 ** (7 - drop))
+    # a weight's rounding, its score's (drop times 8 steps of 32 bits), the two sums' (all keys, one after the other, each addition half
+    # a step: the terms are equal, so roundings may agree)
+    base.close(out, want, want * (rel + weight + (8 * drop + many) * base.U32), "small weights")
