@@ -30,6 +30,9 @@ struct AttnParams {
 // Floats of one split's partial result: maxima and sums of the rows, then their unnormalised outputs.
 inline __host__ __device__ int part_floats(int dim) { return kAttnRows * (dim + 2); }
 
+// Units of n rows, n a power of two; not by a sum or a unit's last row, which may leave 31 bits.
+inline __host__ __device__ constexpr int units_of(int rows, int n) { return rows / n + (rows % n != 0); }
+
 // Rows of a unit where there are many, and the same of such a unit.
 inline __host__ __device__ constexpr int chunk_rows(int dim) { return dim > 128 ? 128 : 256; }
 inline __host__ __device__ constexpr int64_t chunk_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }

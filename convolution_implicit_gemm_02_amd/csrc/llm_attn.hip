@@ -180,7 +180,7 @@ __global__ __launch_bounds__(256, QK == CBS_F32 || DS > 4 ? 1 : 2) void attn_row
   __shared__ int s_last;
 
   // blocks of rows beyond those that the grid was made for: the first split takes all their keys
-  for (int rb = block; rb * kAttnRows < s.rows; rb += p.row_blocks) {
+  for (int rb = block; rb < units_of(s.rows, kAttnRows); rb += p.row_blocks) {
     const int splits = rb == block ? p.splits : 1;
     if (split >= splits) break;
     const int r0 = rb * kAttnRows, rows = min(kAttnRows, s.rows - r0);
@@ -583,7 +583,7 @@ __global__ __launch_bounds__(kAttnChunkThreads, 2) void attn_chunk_kernel(const 
   const float scale = p.scale == 0.0f ? 1.0f : __builtin_fabsf(p.scale);
   const uint32_t sign = p.scale < 0.0f ? 0x80008000u : 0u, whole = p.scale == 0.0f ? 0u : ~0u;
 
-  for (int rb = block; rb * ROWS < s.rows; rb += p.row_blocks) {  // blocks of rows beyond those that the grid was made for: the first split takes all their keys
+  for (int rb = block; rb < units_of(s.rows, ROWS); rb += p.row_blocks) {  // blocks of rows beyond those that the grid was made for: the first split takes all their keys
     const int splits = rb == block ? p.splits : 1;
     if (split >= splits) break;
     const int r0 = rb * ROWS, rows = min(ROWS, s.rows - r0), w0 = r0 + wave * WROWS;

@@ -127,3 +127,19 @@ def test_attn_many_small_weights(kind, new, max_kv, drop, logn):
     # a weight's rounding, its score's (drop times 8 steps of 32 bits), the two sums' (all keys, one after the other, each addition half
     # a step: the terms are equal, so roundings may agree)
     base.close(out, want, want * (rel + weight + (8 * drop + many) * base.U32), "small weights")
+
+
+def test_attn_most_rows_there_can_be():
+    """2^31 - 32768 rows of one sequence (69 GB of outputs): the rows of a block past the last would begin beyond 31 bits."""
+    heads, tokens, dim, page = 65535, 32768, 16, 16
+    q = torch.ones(1, 1, dim, dtype=torch.bfloat16, device="cuda").expand(tokens, heads, dim)
+    k, v, ks, vs = base.kv_buffers(1, 1, dim, page, "i8", fill=1)
+    v[0, 0, :, 0] = torch.arange(1, dim + 1, dtype=torch.int8, device="cuda")
+    vs.fill_(1.0)
+    attn = llm.cbs_attn_create(llm.make_attn_desc(heads, 1, dim, page, causal=False))
+    out = torch.full((tokens, heads, dim), 77, dtype=torch.bfloat16, device="cuda")
+    starts, one, table = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, tokens], [1], [[0]]))
+    llm.cbs_attn_run(attn, q, starts, one, table, k, v, out, ks, vs, max_new=1)
+    want = v[0, 0, :, 0].to(out.dtype)
+    for part in out.split(1024):
+        assert (part == want).all()
