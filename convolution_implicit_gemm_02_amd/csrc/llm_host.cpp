@@ -25,7 +25,7 @@ struct cbs_attn {
 
 namespace {
 
-constexpr int64_t kMaxRows = 0x7fffffff;  // of one call: a grid's first axis
+constexpr int64_t kMaxRows = 0x7fffffff;  // of one call; more than a launch takes go in several
 constexpr int64_t kMaxSpan = (int64_t)1 << 46;  // elements from a tensor's first to its last, so that byte offsets fit 64 bits
 
 cbs_status refuse(cbs_status st, const char *where, const char *fmt, ...) {

@@ -8,6 +8,9 @@
 
 namespace cbs {
 
+// Threads of a launch along its first axis: fewer than 2^32.
+constexpr int64_t kMaxThreads = 0xffffffff;
+
 // The host side has checked every argument before it launches.
 hipError_t launch_rms_norm(const cbs_rms_desc &d, const cbs_rms_args &a, hipStream_t stream);
 hipError_t launch_kv_write(const cbs_kv_desc &d, const cbs_kv_args &a, hipStream_t stream);

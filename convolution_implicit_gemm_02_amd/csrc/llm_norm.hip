@@ -152,9 +152,22 @@ __global__ __launch_bounds__(CH > 4 ? 1024 : 512) void rms_norm_kernel(const Nor
 template <typename T, bool I8, int WB, int CH>
 hipError_t run(NormParams &p, int chunks, hipStream_t stream) {
   p.waves = (chunks + 64 * CH - 1) / (64 * CH);
-  const unsigned grid = (unsigned)(p.waves == 1 ? (p.a.rows + 3) / 4 : p.a.rows);
-  hipLaunchKernelGGL((rms_norm_kernel<T, I8, WB, CH>), dim3(grid), dim3(p.waves == 1 ? 256 : p.waves * 64), 0, stream, p);
-  return hipGetLastError();
+  const int threads = p.waves == 1 ? 256 : p.waves * 64, rows = p.waves == 1 ? 4 : 1;  // of a workgroup
+  const cbs_rms_args &a = p.a;
+  const int64_t most = kMaxThreads / threads * rows;
+  for (int64_t row = 0; row < a.rows; row += most) {
+    NormParams q = p;
+    q.a.rows = a.rows - row < most ? a.rows - row : most;
+    q.a.x = (const T *)a.x + row * a.x_stride;
+    if (a.residual) q.a.residual = (const T *)a.residual + row * a.residual_stride;
+    if (a.residual_out) q.a.residual_out = (T *)a.residual_out + row * a.residual_out_stride;
+    q.a.out = (char *)a.out + row * a.out_stride * (I8 ? 1 : (int)sizeof(T));
+    if (I8) q.a.out_scale = a.out_scale + row;
+    hipLaunchKernelGGL((rms_norm_kernel<T, I8, WB, CH>), dim3((unsigned)((q.a.rows + rows - 1) / rows)), dim3(threads), 0, stream, q);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Chunks of a thread: one where few rows leave the compute units idle, so that a row is read in one step; else two, so that

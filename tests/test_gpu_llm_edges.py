@@ -143,3 +143,25 @@ def test_attn_most_rows_there_can_be():
     want = v[0, 0, :, 0].to(out.dtype)
     for part in out.split(1024):
         assert (part == want).all()
+
+
+# ---------------------------------------------------------------- more than one launch takes
+
+
+@pytest.mark.parametrize("out", ["same", "i8"])
+def test_norm_rows_past_one_launch(out):
+    """2^26 + 1029 rows of a wave each: 2^32 threads and more."""
+    rows, dim, part = (1 << 26) + 1029, 8, 1 << 24
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, r = (torch.randn(rows, dim, generator=g, device="cuda").bfloat16() for _ in range(2))
+    w = (1 + 0.2 * torch.randn(dim, generator=g, device="cuda")).bfloat16()
+    y = torch.full((rows, dim), 77, dtype=torch.int8 if out == "i8" else torch.bfloat16, device="cuda")
+    h, step = torch.full_like(x, 77), torch.full((rows,), 77.0, device="cuda") if out == "i8" else None
+    desc = llm.make_rms_desc(dim, out_dtype=KIND[out if out == "i8" else "bf16"])
+    llm.cbs_rms_norm(desc, x, w, y, residual=r, residual_out=h, out_scale=step)
+    got = [torch.empty_like(t[:part]) if t is not None else None for t in (y, h, step)]
+    for at in range(0, rows, part):  # parts of the same, of one launch each: the same bits
+        n = min(part, rows - at)
+        a, b, c = (None if t is None else t[:n] for t in got)
+        llm.cbs_rms_norm(desc, x[at : at + n], w, a, residual=r[at : at + n], residual_out=b, out_scale=c)
+        assert torch.equal(y[at : at + n], a) and torch.equal(h[at : at + n], b) and (c is None or torch.equal(step[at : at + n], c)), at
