@@ -78,6 +78,7 @@ __global__ __launch_bounds__(256) void kv_kernel(const KvParams p) {
 //          8192:         6.2 | 7.5, 13.5 | 9.6;    6.3 | 12.1, 25 | 27;  16384: 6.8 | 12.1, 16.7 | 18.0;  10.6 | 21.5, 45 | 53
 constexpr int kTile = 16;
 constexpr int64_t kManyVectors = 8192;
+constexpr int64_t kMostVectors = 1 << 29;  // of a launch: a wave has 16, 2^31 threads in all
 
 // A tile's slots, the same in all waves of its heads.
 struct Slots {
@@ -417,18 +418,26 @@ hipError_t run_tile(const KvParams &p, hipStream_t stream) {
 
 template <bool WRITE>
 hipError_t run(const cbs_kv_desc &d, const cbs_kv_args &a, hipStream_t stream) {
-  const KvParams p = {d, a, make_fastdiv(d.heads), make_fastdiv(d.page_size), a.pages >= ((int64_t)1 << 31) / d.page_size};
-  if (a.tokens * d.heads >= kManyVectors && a.tokens * d.heads <= (1 << 30)) {  // tiles are counted in 31 bits
-    const int kind = WRITE ? d.dtype : d.read_dtype;
-    if (d.cache_dtype == CBS_I8) {
-      if (kind == CBS_F16) return run_tile<WRITE, f16_t, true>(p, stream);
-      if (kind == CBS_BF16) return run_tile<WRITE, bf16_t, true>(p, stream);
-      return run_tile<WRITE, float, true>(p, stream);
-    }
-    return kind == CBS_F16 ? run_tile<WRITE, f16_t, false>(p, stream) : run_tile<WRITE, bf16_t, false>(p, stream);
+  KvParams p = {d, a, make_fastdiv(d.heads), make_fastdiv(d.page_size), a.pages >= ((int64_t)1 << 31) / d.page_size};
+  const int kind = WRITE ? d.dtype : d.read_dtype, size = kind == CBS_F32 ? 4 : 2;
+  if (a.tokens * d.heads < kManyVectors) {
+    hipLaunchKernelGGL(kv_kernel<WRITE>, dim3((unsigned)((a.tokens * d.heads + 3) / 4), 2), dim3(256), 0, stream, p);
+    return hipGetLastError();
   }
-  hipLaunchKernelGGL(kv_kernel<WRITE>, dim3((unsigned)((a.tokens * d.heads + 3) / 4), 2), dim3(256), 0, stream, p);
-  return hipGetLastError();
+  const int64_t most = kMostVectors / d.heads / kTile * kTile;  // whole tiles: 65535 heads have some
+  for (int64_t token = 0; token < a.tokens; token += most) {
+    p.a.tokens = a.tokens - token < most ? a.tokens - token : most;
+    p.a.slots = a.slots + token;
+    p.a.k = (char *)a.k + token * a.k_token_stride * size;
+    p.a.v = (char *)a.v + token * a.v_token_stride * size;
+    hipError_t e;
+    if (d.cache_dtype != CBS_I8) e = kind == CBS_F16 ? run_tile<WRITE, f16_t, false>(p, stream) : run_tile<WRITE, bf16_t, false>(p, stream);
+    else if (kind == CBS_F16) e = run_tile<WRITE, f16_t, true>(p, stream);
+    else if (kind == CBS_BF16) e = run_tile<WRITE, bf16_t, true>(p, stream);
+    else e = run_tile<WRITE, float, true>(p, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace

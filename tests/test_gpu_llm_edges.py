@@ -165,3 +165,29 @@ def test_norm_rows_past_one_launch(out):
         a, b, c = (None if t is None else t[:n] for t in got)
         llm.cbs_rms_norm(desc, x[at : at + n], w, a, residual=r[at : at + n], residual_out=b, out_scale=c)
         assert torch.equal(y[at : at + n], a) and torch.equal(h[at : at + n], b) and (c is None or torch.equal(step[at : at + n], c)), at
+
+
+def test_kv_vectors_past_one_launch():
+    """2^30 vectors and more (69 GB read back), of which all but a few tokens, at the ends of launches, have no slot."""
+    heads, dim, page, tokens = 65535, 16, 16, 16400
+    good = list(range(5)) + list(range(8186, 8198)) + list(range(16381, 16389)) + list(range(tokens - 4, tokens))
+    slots = torch.full((tokens,), -1, dtype=torch.int64)
+    slots[good] = torch.arange(len(good)) + 7
+    slots = slots.cuda()
+    g = base.gen(4)
+    k, v = (base.normal(g, tokens, 1, dim, kind="bf16").cuda().expand(tokens, heads, dim) for _ in range(2))
+    kc, vc, ks, vs = base.kv_buffers(3, heads, dim, page, "i8")
+    desc = llm.make_kv_desc(heads, dim, page)
+    llm.cbs_kv_write(desc, k, v, slots, kc, vc, ks, vs)
+    want = base.kv_buffers(3, heads, dim, page, "i8")  # the same of the few tokens alone: one launch
+    llm.cbs_kv_write(desc, k[good], v[good], slots[good], *want)
+    for a, b in zip((kc, vc, ks, vs), want):
+        assert torch.equal(a, b)
+    out = [torch.full((tokens, heads, dim), 77, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    llm.cbs_kv_read(desc, slots, kc, vc, out[0], out[1], ks, vs)
+    few = [torch.empty(len(good), heads, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    llm.cbs_kv_read(desc, slots[good], kc, vc, few[0], few[1], ks, vs)
+    for a, b in zip(out, few):
+        assert torch.equal(a[good], b)
+        a[good] = 0
+        assert not any(part.any() for part in a.split(1024))
