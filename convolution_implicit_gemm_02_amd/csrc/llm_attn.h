@@ -12,6 +12,7 @@ constexpr int kAttnRows = 16;         // rows of a unit: the columns of one matr
 constexpr int kAttnMaxSplits = 32;
 constexpr int kAttnMaxParts = 1024;   // workgroups of a call whose units are split: as many partial results are kept
 constexpr int kAttnMaxChunkParts = 256;
+constexpr int kAttnThreads = 256, kAttnChunkThreads = 512;  // of a workgroup: units of 16 rows, of many
 
 struct AttnParams {
   cbs_attn_args a;

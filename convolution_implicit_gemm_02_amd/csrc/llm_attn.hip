@@ -157,7 +157,7 @@ __device__ __forceinline__ int page_of(const AttnParams &p, const Seq &s, int b,
 // heads over 8 of int8 and 8192 tokens: 94 us, 4.6 TB/s; one sequence over 1000 tokens: 12.6 us, of which the data is 1: lengths,
 // pages, keys, values, and the join of the splits, one after the other.
 template <int QK, int CK, int DS, bool PAD>
-__global__ __launch_bounds__(256, QK == CBS_F32 || DS > 4 ? 1 : 2) void attn_rows_kernel(const AttnParams p) {
+__global__ __launch_bounds__(kAttnThreads, QK == CBS_F32 || DS > 4 ? 1 : 2) void attn_rows_kernel(const AttnParams p) {
   constexpr bool I8 = CK == CBS_I8, SF16 = QK == CBS_F16, PF16 = CK == CBS_F16;
   // float32 queries and weights as three bfloat16 terms, all 24 bits; float16 rows on int8 values: weight times the value's
   // step leaves float16's range, so two bfloat16 terms; else the weights are rounded once to the 16-bit type
@@ -496,8 +496,6 @@ __global__ __launch_bounds__(256, QK == CBS_F32 || DS > 4 ? 1 : 2) void attn_row
     if (threadIdx.x == 0) __hip_atomic_store(p.tickets + unit, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
-
-constexpr int kAttnChunkThreads = 512;
 
 // LDS of a unit of many rows, in bytes.
 template <bool I8, int DS>
@@ -1033,7 +1031,7 @@ hipError_t run_chunk(const AttnParams &p, unsigned grid, hipStream_t stream) {
 
 template <int DS, bool PAD>
 hipError_t run_rows(const AttnParams &p, unsigned grid, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_rows_kernel<kPairQ[CBS_ATTN_PAIR], kPairC[CBS_ATTN_PAIR], DS, PAD>), dim3(grid), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL((attn_rows_kernel<kPairQ[CBS_ATTN_PAIR], kPairC[CBS_ATTN_PAIR], DS, PAD>), dim3(grid), dim3(kAttnThreads), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -114,10 +114,12 @@ void cut(const cbs_attn_desc &d, const cbs_attn_args &a, AttnParams *p) {
   const int64_t rows = std::min<int64_t>(a.max_new, a.tokens) * p->group, seqs_heads = (int64_t)a.seqs * d.kv_heads;
   int64_t keys = std::min<int64_t>(a.max_kv, (int64_t)a.columns * d.page_size);
   if (d.window > 0 && d.causal) keys = std::min<int64_t>(keys, (int64_t)d.window + a.max_new);
-  const int64_t blocks = (rows + kAttnRows - 1) / kAttnRows, most_blocks = ((int64_t)1 << 24) / seqs_heads;
+  const int64_t blocks = (rows + kAttnRows - 1) / kAttnRows;
   const double work = (double)(seqs_heads * blocks) * std::max<double>(0, keys - (d.causal ? a.max_new / 2 : 0)) * d.head_dim / 128 * (d.cache_dtype == CBS_I8 ? 0.6 : 1.0);
   const bool dims = d.head_dim == 64 || d.head_dim == 96 || d.head_dim == 128 || d.head_dim == 256;
   p->chunk = dims && d.dtype != CBS_F32 && rows * 5 >= chunk_rows(d.head_dim) * 2 && work >= 150e3;
+  // what a launch takes; a workgroup goes on to the blocks of rows behind them
+  const int64_t most_blocks = kMaxThreads / (p->chunk ? kAttnChunkThreads : kAttnThreads) / seqs_heads;
   if (p->chunk) {
     p->row_blocks = (int)std::max<int64_t>(1, std::min((rows + chunk_rows(d.head_dim) - 1) / chunk_rows(d.head_dim), most_blocks));
     const int64_t units = seqs_heads * p->row_blocks;
@@ -345,7 +347,6 @@ cbs_status cbs_attn_run(const cbs_attn *attn, const cbs_attn_args *a, void *stre
   int device = -1;
   if (hipGetDevice(&device) != hipSuccess || device != attn->device) return refuse(CBS_EINVAL, where, "the handle belongs to device %d", attn->device);
   AttnParams p = {};
-  p.a = *a;
   p.dim = d.head_dim;
   p.page = d.page_size;
   p.kv_heads = d.kv_heads;
@@ -353,15 +354,23 @@ cbs_status cbs_attn_run(const cbs_attn *attn, const cbs_attn_args *a, void *stre
   p.causal = d.causal;
   p.window = d.window;
   p.scale = d.scale * 1.44269504088896340736f;
-  cut(d, *a, &p);
   p.by_page = make_fastdiv(p.page);
   p.by_group = make_fastdiv(p.group);
-  p.by_splits = make_fastdiv(p.splits);
-  p.by_row_blocks = make_fastdiv(p.row_blocks);
   p.by_kv_heads = make_fastdiv(p.kv_heads);
   p.part = attn->part;
   p.tickets = attn->tickets;
-  return launched(launch_attn(p, d, (hipStream_t)stream), where);
+  const int most = (int)(kMaxThreads / kAttnChunkThreads / d.kv_heads);  // sequences of a launch
+  for (int b = 0; b < a->seqs; b += most) {
+    p.a = *a;
+    p.a.seqs = std::min(a->seqs - b, most);
+    p.a.q_start += b, p.a.kv_len += b, p.a.table += b * a->table_stride;
+    cut(d, p.a, &p);
+    p.by_splits = make_fastdiv(p.splits);
+    p.by_row_blocks = make_fastdiv(p.row_blocks);
+    st = launched(launch_attn(p, d, (hipStream_t)stream), where);
+    if (st != CBS_OK) return st;
+  }
+  return CBS_OK;
 }
 
 void cbs_attn_destroy(cbs_attn *attn) {

@@ -191,3 +191,44 @@ def test_kv_vectors_past_one_launch():
         assert torch.equal(a[good], b)
         a[good] = 0
         assert not any(part.any() for part in a.split(1024))
+
+
+def many_sequences(seqs, heads, kv_heads, dim, kind, seed):
+    """A new token each, over two pages that they share."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    page = 16
+    q = torch.randn(seqs, heads, dim, generator=g, device="cuda").to(base.TYPES[kind])
+    k, v = (torch.randint(-127, 128, shape, generator=g, device="cuda", dtype=torch.int8) for shape in ((2, kv_heads, page, dim), (2, kv_heads, dim, page)))
+    ks, vs = ((0.5 + torch.rand(2, kv_heads, page, generator=g, device="cuda")) / 70 for _ in range(2))
+    kv_len = torch.randint(0, 33, (seqs,), generator=g, device="cuda", dtype=torch.int32)
+    table = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda").repeat(seqs, 1)
+    return q, torch.arange(seqs + 1, dtype=torch.int32, device="cuda"), kv_len, table, k, v, ks, vs
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_attn_sequences_past_one_launch(kind):
+    """65535 sequences over 512 heads of the cache: 2^25 units."""
+    seqs, heads, dim, part = 65535, 512, 16, 8000
+    q, q_start, kv_len, table, k, v, ks, vs = many_sequences(seqs, heads, heads, dim, kind, 6)
+    attn = llm.cbs_attn_create(llm.make_attn_desc(heads, heads, dim, 16, dtype=KIND[kind], max_seqs=seqs))
+    out = torch.full_like(q, 77)
+    llm.cbs_attn_run(attn, q, q_start, kv_len, table, k, v, out, ks, vs, max_new=1)
+    few = torch.empty_like(q[:part])
+    for at in range(0, seqs, part):  # parts of the same, of one launch each: the same bits
+        n = min(part, seqs - at)
+        llm.cbs_attn_run(attn, q[at : at + n], q_start[: n + 1], kv_len[at : at + n], table[at : at + n], k, v, few[:n], ks, vs, max_new=1)
+        assert torch.equal(out[at : at + n], few[:n]), at
+
+
+@pytest.mark.parametrize("kind,heads,dim", [("bf16", 512, 64), ("f16", 512, 64), ("f32", 64, 64), ("bf16", 64, 48)])
+def test_attn_bounds_past_one_launch(kind, heads, dim):
+    """max_new as if all tokens were one sequence's: units of 2^32 threads and more, of many rows and of 16."""
+    seqs = 2048
+    q, q_start, kv_len, table, k, v, ks, vs = many_sequences(seqs, heads, 1, dim, kind, 7)
+    attn = llm.cbs_attn_create(llm.make_attn_desc(heads, 1, dim, 16, dtype=KIND[kind], causal=False, max_seqs=seqs))
+    out = torch.full_like(q, 77), torch.full_like(q, 78)
+    for to, most in zip(out, (seqs, 1)):
+        llm.cbs_attn_run(attn, q, q_start, kv_len, table, k, v, to, ks, vs, max_new=most)
+    assert torch.equal(*out)
+    want, mags, tops = ref.attention(*(t.cpu() for t in (q[:5], q_start[:6], kv_len[:5], table[:5], k, v)), dim ** -0.5, False, 0, ks.cpu(), vs.cpu())
+    base.close(out[0][:5], want, base.attn_bound(want, mags, tops, kind, dim, 32), "of the first")
