@@ -222,7 +222,7 @@ struct Weights {
 // A block's products with RB blocks of 16 rows; x_at(s, m, t): fragment s (int8: of two steps) of row block m, term t.
 // SUMS: codes as they are, less the zero point times the rows' own sums -- 7 instructions for eight codes rather than 11
 // (float16) or 16 (bfloat16), for one more product a fragment and a step's end that is twice as long, so for one block of rows
-// only.  Errors are those of sum |x| (code + zero) in place of sum |x| |code - zero|, in 32 bits.  Not for infinities.
+// only.  Errors are those of sum |x| (code + zero) in place of sum |x| |code - zero|, in 32 bits.  Not for what wild_of() finds.
 // OWN: x lies in its own order (int8: 16 bytes of a lane are neighbours, so that a group of 32 is two of the lanes' groups).
 template <bool ZEROS, bool SUMS, bool OWN, int RB, int NB, int GS, bool WIDE, typename XAt>
 __device__ __forceinline__ void multiply(const Weights<NB, GS, WIDE> &ws, typename Weights<NB, GS, WIDE>::Block &w, const XAt &x_at, f32x4 (&total)[NB][RB]) {
@@ -387,9 +387,10 @@ __device__ __forceinline__ void join(const W4Params &p, f32x4 (&total)[NB][RB], 
   }
 }
 
-// Of two 16-bit floats, one is infinite or NaN.
-[[maybe_unused]] __device__ __forceinline__ bool infinite(uint32_t two) {
-  constexpr uint32_t E = X == X_F16 ? 0x7c00u : 0x7f80u;
+// Of two 16-bit floats, one is infinite or NaN, or as a bfloat16 2^97 and more: the sums of 2^16 such times codes and zero points
+// would leave 32 bits where those of their differences need not.
+[[maybe_unused]] __device__ __forceinline__ bool wild_of(uint32_t two) {
+  constexpr uint32_t E = X == X_F16 ? 0x7c00u : 0x7000u;
   return (two & E) == E || (two & E << 16) == E << 16;
 }
 
@@ -422,12 +423,12 @@ __global__ __launch_bounds__(kW4Waves * 64) void w4_few_kernel(const W4Params p)
   constexpr bool SUMS = X == X_F16 || X == X_BF16;
   constexpr int BATCH = X == X_F32 ? 2 : X == X_I8 ? 8 : 4;
   __shared__ int s_wild[kW4Waves];
-  bool wild = false;  // an infinity or NaN
+  bool wild = false;  // see wild_of()
   const int whole = p.k / 8, rest = p.blocks * 16 - whole;  // pieces of a row
   const auto put = [&](const Piece &v, int m, int q) {
     if constexpr (SUMS) {
 #pragma unroll
-      for (int j = 0; j < 4; j++) wild |= infinite(v.w[j]);
+      for (int j = 0; j < 4; j++) wild |= wild_of(v.w[j]);
     }
     write_piece<GS>(v, lds + (q >> 4) * stage, q & 15, m, r, 1);
   };
@@ -484,7 +485,7 @@ __global__ __launch_bounds__(kW4Waves * 64) void w4_few_kernel(const W4Params p)
   if constexpr (!SUMS) return;
   int any = 0;
   for (int i = 0; i < threads / 64; i++) any |= s_wild[i];
-  if (any) {  // rare: a wave an output, as the formula has it
+  if (any) {  // rare: a wave an output, as the formula has it, times 2^-8: no product of x and a whole number leaves 32 bits
     __syncthreads();
     for (int e = wave; e < rows * tile_n; e += threads / 64) {
       const int m = e / tile_n, n = tile * tile_n + e % tile_n;
@@ -494,9 +495,10 @@ __global__ __launch_bounds__(kW4Waves * 64) void w4_few_kernel(const W4Params p)
       for (int k = lane; k < p.k; k += 64) {
         const int64_t at = (int64_t)(k / p.group) * p.n + n;
         const int c = (codes[k / 2] >> (4 * (k & 1)) & 15) - (ws.has_zeros ? p.a.zeros[at] : 8);
-        sum = __builtin_fmaf(load_as_f32(p.a.x, m * p.a.x_stride + k, X == X_F16 ? CBS_F16 : CBS_BF16) * (float)c, load_as_f32(p.a.scales, at, p.scale_dtype), sum);
+        const float x = load_as_f32(p.a.x, m * p.a.x_stride + k, X == X_F16 ? CBS_F16 : CBS_BF16) * 0x1p-8f;
+        sum = __builtin_fmaf(x * (float)c, load_as_f32(p.a.scales, at, p.scale_dtype), sum);
       }
-      sum = wave_sum(sum);
+      sum = wave_sum(sum) * 0x1p8f;
       if (lane == 0) store_f32_as(p.a.out, m * p.a.out_stride + n, sum, p.out_dtype);
     }
   }

@@ -12,6 +12,8 @@
  * 4-bit linear, groups g of `group` consecutive input features:
  *   y[m][n] = x_scale[m] * sum_g scales[g][n] * sum_{k in g} x[m][k] * (code[n][k] - zero[g][n])
  *   x_scale is 1 for floating rows; zero is 8 where none are given.
+ *   The sums of x (code - zero) over 128 input features, times 16, are 32-bit floats: an |x| of 2^108 and more may overflow them
+ *   (bfloat16 on few rows: not before the formula's own do).
  * Paged cache, of keys and values of `heads` heads:  slot = page * page_size + place;  a token's vector v of one head is kept as
  *   s = fp32(max_i |v_i| / 127), 1 where that is 0,  q_i = clamp(rne(fp32(v_i / s)), -127, 127)   (cache_dtype CBS_I8)
  *   or as it is (cache_dtype CBS_F16 or CBS_BF16), and read back as T(fp32(q_i * s)) or as it is.

@@ -35,6 +35,27 @@ def test_w4_group_longer_than_k(kind, rows, k, group):
     assert torch.isfinite(out[0]).all() and torch.equal(*out)
 
 
+
+@pytest.mark.parametrize("rows,k", [(1, 4096), (3, 250), (16, 512)])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("by", [2.0 ** 95, 2.0 ** 113])
+def test_w4_large_bfloat16(rows, k, zeros, by):
+    """Inputs near the type's end, whose weighted sum 32 bits hold, and rows of other sizes beside them."""
+    g = base.gen(k)
+    n, group = 50, 64
+    packed = torch.randint(0, 256, (n, (k + 31) // 32 * 16), generator=g, dtype=torch.uint8)
+    sc = (0.5 + torch.rand(-(-k // group), n, generator=g)) * 2.0 ** -12
+    z = torch.randint(0, 16, sc.shape, generator=g, dtype=torch.uint8) if zeros else None
+    x = base.normal(g, rows, k, kind="bf16", by=by)
+    x[rows // 2] = base.normal(g, k, kind="bf16")
+    x[0, k // 2] = 2.0 ** 126
+    out = torch.full((rows, n), math.nan, device="cuda")
+    llm.cbs_w4_linear(llm.make_w4_desc(k, n, group, out_dtype=llm.CBS_F32, scale_dtype=llm.CBS_F32), x.cuda(), packed.cuda(), sc.cuda(), out, zeros=z.cuda() if zeros else None)
+    y, mag = ref.w4_linear(x, packed, sc, group, z)
+    _, sums = ref.w4_linear(x.abs(), packed, sc, group, torch.zeros_like(sc, dtype=torch.uint8))
+    base.close(out, y, (mag + 2 * sums) * (k + sc.shape[0] + 4) * base.U32 + y.abs() * base.U32, "large")
+
+
 # ---------------------------------------------------------------- attention
 
 
