@@ -608,7 +608,8 @@ __global__ __launch_bounds__(kAttnChunkThreads, 2) void attn_chunk_kernel(const 
       }
     }
     f32x4 o[RB][DB];
-    float top[RB], l[RB];
+    constexpr float UP = PF16 ? 7.0f : 0.0f;  // weights up to 2^8, float16 2^15
+    float top[RB], l[RB];                     // the maximum, less UP
 #pragma unroll
     for (int m = 0; m < RB; m++) {
       top[m] = -INFINITY, l[m] = 0.0f;
@@ -737,11 +738,13 @@ __global__ __launch_bounds__(kAttnChunkThreads, 2) void attn_chunk_kernel(const 
         const int next = slot + 1 == L::SLOTS ? 0 : slot + 1, last = slot == 0 ? L::SLOTS - 1 : slot - 1;
         const int spare = !LATE ? last : last == 0 ? L::SLOTS - 1 : last - 1;  // the slot that no tile needs any more
         f32x4 step_k[2], step_v[2];  // int8: of the lane's keys
+        [[maybe_unused]] float step_one = 0.0f;  // of the tile's values, a lane's own
         if constexpr (I8) {
           // tile t + 1 is in its slot once all waves are here; t + 2's codes go to the spare one, and t + AHEAD's to where t's were
           const unsigned char *steps = lds + L::RAW + raw * L::RAW_SLOT + L::RAW_STEPS + wave * 256 + 32 * g;
           step_k[0] = *(const f32x4 *)steps, step_k[1] = *(const f32x4 *)(steps + 16);
           step_v[0] = *(const f32x4 *)(steps + 128), step_v[1] = *(const f32x4 *)(steps + 144);
+          if (NP > 1) step_one = *(const float *)(lds + L::RAW + raw * L::RAW_SLOT + L::RAW_STEPS + wave * 256 + 128 + (lane & 31) * 4);
           wait_vm<OPS *(AHEAD - 3)>();
           lds_barrier();
           const int raw2 = raw + 2 >= AHEAD ? raw + 2 - AHEAD : raw + 2;
@@ -806,7 +809,7 @@ __global__ __launch_bounds__(kAttnChunkThreads, 2) void attn_chunk_kernel(const 
         }
         if constexpr (I8) {
           // Values' steps that are infinite or NaN: hidden ones must not meet a weight of zero, and none can be taken apart in two terms.
-          if (edge || NP > 1) {
+          if (edge || (NP > 1 && __any(!__builtin_isfinite(step_one)))) {
             bool any = false;
 #pragma unroll
             for (int i = 0; i < 8; i++)
@@ -817,7 +820,7 @@ __global__ __launch_bounds__(kAttnChunkThreads, 2) void attn_chunk_kernel(const 
         float most[RB];
         bool rise = false, none = t == t0;  // none: no weights are due
 #pragma unroll
-        for (int m = 0; m < RB; m++) most[m] = most_of(sc[m]) * by, rise |= most[m] > top[m] + 8.0f;
+        for (int m = 0; m < RB; m++) most[m] = most_of(sc[m]) * by, rise |= most[m] > top[m] + (8.0f + UP);
         if (__any(rise)) {
           if constexpr (LATE) {  // what is due, at the old maxima
             if (!none) {
@@ -830,7 +833,7 @@ __global__ __launch_bounds__(kAttnChunkThreads, 2) void attn_chunk_kernel(const 
           for (int m = 0; m < RB; m++) {
             most[m] = fmaxf(most[m], __shfl_xor(most[m], 16));
             most[m] = fmaxf(most[m], __shfl_xor(most[m], 32));
-            const float up = fmaxf(top[m], most[m]), less = top[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top[m] - up);
+            const float up = fmaxf(top[m], most[m] - UP), less = top[m] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top[m] - up);
             top[m] = up;
             l[m] *= less;
 #pragma unroll
@@ -874,7 +877,7 @@ __global__ __launch_bounds__(kAttnChunkThreads, 2) void attn_chunk_kernel(const 
         }
         float from[RB];
 #pragma unroll
-        for (int m = 0; m < RB; m++) from[m] = top[m] == -INFINITY ? 0.0f : (PF16 ? 7.0f : 0.0f) - top[m];  // weights up to 2^8, float16 2^15
+        for (int m = 0; m < RB; m++) from[m] = top[m] == -INFINITY ? 0.0f : -top[m];
 
         // pair i of the tile's weights: two keys of a row
         f32x4 sc2[RB][2];
