@@ -168,7 +168,7 @@ PyObject *attn_run(PyObject *, PyObject *const *args, Py_ssize_t n) {
   a.v_scale = (const float *)c.at(10, at::kFloat, {pages, d.kv_heads, d.page_size}, true, true);
   void *handle = PyLong_Check(args[0]) ? PyLong_AsVoidPtr(args[0]) : nullptr;
   long most[2];
-  const int64_t all[2] = {tokens, columns * d.page_size};
+  const int64_t all[2] = {tokens == seqs ? 1 : tokens, columns * d.page_size};
   for (int i = 0; i < 2; i++) {
     int over = 0;
     most[i] = args[11 + i] == Py_None ? (long)all[i] : PyLong_Check(args[11 + i]) ? PyLong_AsLongAndOverflow(args[11 + i], &over) : -1;

@@ -253,3 +253,44 @@ def test_attn_bounds_past_one_launch(kind, heads, dim):
     assert torch.equal(*out)
     want, mags, tops = ref.attention(*(t.cpu() for t in (q[:5], q_start[:6], kv_len[:5], table[:5], k, v)), dim ** -0.5, False, 0, ks.cpu(), vs.cpu())
     base.close(out[0][:5], want, base.attn_bound(want, mags, tops, kind, dim, 32), "of the first")
+
+
+# ---------------------------------------------------------------- what the bindings pass
+
+
+@pytest.fixture
+def passed(monkeypatch):
+    """Arguments of cbs_attn_run, from the extension module and from the checks in Python, in place of a run."""
+    import ctypes
+    from types import SimpleNamespace
+    got = []
+
+    def take(attn, args, stream):
+        got.append(llm.cbs_attn_args.from_buffer_copy(ctypes.string_at(args, ctypes.sizeof(llm.cbs_attn_args))))
+        return 0
+
+    names = ("cbs_rms_norm", "cbs_w4_linear", "cbs_kv_write", "cbs_kv_read", "cbs_attn_run")
+    addresses = [ctypes.cast(getattr(llm.lib, name), ctypes.c_void_p).value for name in names]
+    called = ctypes.CFUNCTYPE(ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p)(take)
+    llm._llm_bind.setup(*addresses[:4], ctypes.cast(called, ctypes.c_void_p).value)
+    monkeypatch.setattr(llm, "lib", SimpleNamespace(cbs_attn_run=lambda attn, args, stream: take(attn, args, stream), cbs_attn_destroy=llm.lib.cbs_attn_destroy))
+    yield got
+    llm._llm_bind.setup(*addresses)
+
+
+@pytest.mark.parametrize("tokens,seqs,most", [(32, 32, 1), (32, 1, 32), (543, 32, 543), (5, 9, 5), (1, 1, 1), (0, 3, 0)])
+def test_attn_default_of_max_new(passed, tokens, seqs, most):
+    """As many as there are, but for a batch of single tokens."""
+    attn = llm.Attn(0, llm.make_attn_desc(2, 1, 16, 16, max_seqs=seqs))
+    attn.handle = 1  # no run uses it
+    try:
+        q = torch.zeros(tokens, 2, 16, dtype=torch.bfloat16, device="cuda")
+        caches = base.kv_buffers(2, 1, 16, 16, "i8")
+        starts, lengths = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (seqs + 1, seqs))
+        table = torch.zeros(seqs, 3, dtype=torch.int32, device="cuda")
+        for stream in (None, torch.cuda.current_stream()):
+            llm.cbs_attn_run(attn, q, starts, lengths, table, caches[0], caches[1], q, caches[2], caches[3], stream=stream)
+            llm.cbs_attn_run(attn, q, starts, lengths, table, caches[0], caches[1], q, caches[2], caches[3], max_new=7, max_kv=9, stream=stream)
+    finally:
+        attn.handle = 0
+    assert [(a.max_new, a.max_kv) for a in passed] == [(most, 48), (7, 9)] * 2
