@@ -2,6 +2,7 @@
 // little cost to the host.  It looks at the same things as llm.py and never decides that something is wrong: it returns -1,
 // and llm.py says what.  A call of one token costs the GPU 2 to 10 us; from Python statements alone the host needs 8, so 5.
 #include <Python.h>
+#include <algorithm>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -168,7 +169,7 @@ PyObject *attn_run(PyObject *, PyObject *const *args, Py_ssize_t n) {
   a.v_scale = (const float *)c.at(10, at::kFloat, {pages, d.kv_heads, d.page_size}, true, true);
   void *handle = PyLong_Check(args[0]) ? PyLong_AsVoidPtr(args[0]) : nullptr;
   long most[2];
-  const int64_t all[2] = {tokens == seqs ? 1 : tokens, columns * d.page_size};
+  const int64_t all[2] = {tokens == seqs ? 1 : tokens, std::min<int64_t>(columns * d.page_size, 0x7fffffff)};
   for (int i = 0; i < 2; i++) {
     int over = 0;
     most[i] = args[11 + i] == Py_None ? (long)all[i] : PyLong_Check(args[11 + i]) ? PyLong_AsLongAndOverflow(args[11 + i], &over) : -1;

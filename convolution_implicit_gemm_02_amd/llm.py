@@ -260,4 +260,4 @@ def cbs_attn_run(attn: Attn, q, q_start, kv_len, table, k_cache, v_cache, out, k
         _dense(v_cache, "v_cache", attn.kept, cache + (dim, page), dev), 0 if k_scale is None else _dense(k_scale, "k_scale", torch.float32, per, dev),
         0 if v_scale is None else _dense(v_scale, "v_scale", torch.float32, per, dev), _ptr(out, "out", attn.kind, shape, dev),
         tokens, pages, q.stride(0), q.stride(1), out.stride(0), out.stride(1), table.stride(0), seqs, columns,
-        (1 if tokens == seqs else tokens) if max_new is None else max_new, columns * page if max_kv is None else max_kv), _stream(stream, dev)), "cbs_attn_run")
+        (1 if tokens == seqs else tokens) if max_new is None else max_new, min(columns * page, 2**31 - 1) if max_kv is None else max_kv), _stream(stream, dev)), "cbs_attn_run")

@@ -294,3 +294,31 @@ def test_attn_default_of_max_new(passed, tokens, seqs, most):
     finally:
         attn.handle = 0
     assert [(a.max_new, a.max_kv) for a in passed] == [(most, 48), (7, 9)] * 2
+
+
+def test_attn_default_of_max_kv(passed):
+    """A table with room for 2^31 tokens and more."""
+    attn = llm.Attn(0, llm.make_attn_desc(1, 1, 16, 1024))
+    attn.handle = 1  # no run uses it
+    try:
+        q = torch.zeros(2, 1, 16, dtype=torch.bfloat16, device="cuda")
+        caches = base.kv_buffers(2, 1, 16, 1024, "i8")
+        starts, lengths = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (2, 1))
+        for columns, most in ((1 << 21, 2**31 - 1), ((1 << 21) - 1, 2**31 - 1024)):
+            table = torch.zeros(1, columns, dtype=torch.int32, device="cuda")
+            for stream in (None, torch.cuda.current_stream()):
+                llm.cbs_attn_run(attn, q, starts, lengths, table, caches[0], caches[1], q, caches[2], caches[3], stream=stream)
+                assert (passed[-1].max_new, passed[-1].max_kv) == (2, most)
+    finally:
+        attn.handle = 0
+    assert len(passed) == 4
+
+
+def test_attn_table_past_31_bits():
+    """The run itself with such a table."""
+    made = list(base.make_attn([1, 3], [40, 40], 2, 1, 16, 1024, "bf16", "i8"))
+    want = base.run_attn(made, 2, 1, 16, 1024, "bf16", "i8")
+    table = torch.full((2, (1 << 21) + 3), -1, dtype=torch.int32)
+    table[:, :1] = made[3]
+    made[3] = table
+    assert torch.equal(base.run_attn(made, 2, 1, 16, 1024, "bf16", "i8"), want)
