@@ -59,7 +59,7 @@ cbs_status check_heads(const char *where, const char *what, int64_t tokens, int6
   if (head_stride < 0 || token_stride < 0) return refuse(CBS_EINVAL, where, "%s: negative stride", what);
   if ((heads > 1 && head_stride > kMaxSpan / heads) || (tokens > 1 && token_stride > kMaxSpan / tokens))
     return refuse(CBS_EUNSUPPORTED, where, "%s: the tensor is too long", what);
-  if (!out) return CBS_OK;
+  if (!out || tokens == 0) return CBS_OK;
   // of the two axes, the one with the shorter stride lies within one step of the other
   const bool by_token = tokens == 1 || (heads > 1 && token_stride >= head_stride);
   const int64_t inner = by_token ? (heads - 1) * head_stride : (tokens - 1) * token_stride;
@@ -80,11 +80,12 @@ cbs_status check_cache_shape(const char *where, int heads, int head_dim, int pag
 
 cbs_status check_cache(const char *where, const void *k, const void *v, const float *ks, const float *vs, int cache_dtype,
                        int64_t pages, int64_t page_elems) {
+  if (pages < 0) return refuse(CBS_EINVAL, where, "negative pages");
+  if (pages == 0) return CBS_OK;  // its pointers, which may be null, are not looked at
   if (!k || !v) return refuse(CBS_EINVAL, where, "null cache");
   if (!aligned(k, 16) || !aligned(v, 16)) return refuse(CBS_EINVAL, where, "the cache does not begin at a 16-byte boundary");
   if ((cache_dtype == CBS_I8) != (ks != nullptr) || (cache_dtype == CBS_I8) != (vs != nullptr))
     return refuse(CBS_EINVAL, where, "an int8 cache has scales, and no other has");
-  if (pages < 0) return refuse(CBS_EINVAL, where, "negative pages");
   if (pages > kMaxRows || pages > kMaxSpan / page_elems) return refuse(CBS_EUNSUPPORTED, where, "too many pages");
   return CBS_OK;
 }
@@ -337,7 +338,7 @@ cbs_status cbs_attn_run(const cbs_attn *attn, const cbs_attn_args *a, void *stre
   if (a->tokens < 0 || a->columns < 0) return refuse(CBS_EINVAL, where, "negative tokens or columns");
   if (a->tokens > kMaxRows / d.heads) return refuse(CBS_EUNSUPPORTED, where, "too many tokens");
   if (a->max_new < 0 || a->max_kv < 0) return refuse(CBS_EINVAL, where, "max_new %d, max_kv %d", a->max_new, a->max_kv);
-  if (a->seqs > 0 && (!a->q_start || !a->kv_len || !a->table)) return refuse(CBS_EINVAL, where, "null lengths or table");
+  if (a->seqs > 0 && (!a->q_start || !a->kv_len || (!a->table && a->columns > 0))) return refuse(CBS_EINVAL, where, "null lengths or table");
   if (a->seqs > 1 && a->table_stride < a->columns) return refuse(CBS_EINVAL, where, "a table stride of %lld for %d columns", (long long)a->table_stride, a->columns);
   if (a->tokens > 0 && (!a->q || !a->out)) return refuse(CBS_EINVAL, where, "null q or out");
   cbs_status st = check_cache(where, a->k_cache, a->v_cache, a->k_scale, a->v_scale, d.cache_dtype, a->pages, (int64_t)d.kv_heads * d.head_dim * d.page_size);

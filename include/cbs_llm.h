@@ -40,7 +40,8 @@
  *
  * Errors: every entry point returns a cbs_status; cbs_last_error() has a message for the calling thread.  Device data is
  * checked where it is used: a slot outside [0, pages * page_size) is not written and reads as zeros, a page outside
- * [0, pages) in a table hides its keys, lengths are cut at the table's columns.
+ * [0, pages) in a table hides its keys, lengths are cut at the table's columns.  A cache of no pages and a table of no columns
+ * may be NULL.
  */
 #ifndef CBS_LLM_H_
 #define CBS_LLM_H_

@@ -322,3 +322,34 @@ def test_attn_table_past_31_bits():
     table[:, :1] = made[3]
     made[3] = table
     assert torch.equal(base.run_attn(made, 2, 1, 16, 1024, "bf16", "i8"), want)
+
+
+# ---------------------------------------------------------------- empty caches and tables
+
+
+@pytest.mark.parametrize("kind,cache", base.PAIRS)
+@pytest.mark.parametrize("new", [[1, 1], [150, 40]])
+@pytest.mark.parametrize("pages,columns", [(0, 3), (2, 0), (0, 0)])
+def test_attn_of_an_empty_cache(kind, cache, new, pages, columns):
+    """No pages, no columns: no key is seen, whatever the lengths say."""
+    made = list(base.make_attn(new, [200, 64], 4, 2, 64, 16, kind, cache))
+    made[3] = torch.zeros(2, columns, dtype=torch.int32)
+    made[4:] = [None if t is None else t[:pages] for t in made[4:]]
+    for max_kv in (None, 1 << 18):
+        assert (base.run_attn(made, 4, 2, 64, 16, kind, cache, max_kv=max_kv) == 0).all()
+
+
+@pytest.mark.parametrize("kind,cache,read", [("bf16", "i8", "bf16"), ("f16", "f16", "f16"), ("f32", "i8", "f32")])
+@pytest.mark.parametrize("heads", [1, 300])
+def test_kv_of_an_empty_cache(kind, cache, read, heads):
+    """All slots lie outside; reading gives zeros.  And no tokens of a transposed tensor."""
+    kc, vc, ks, vs = base.kv_buffers(0, heads, 64, 16, cache)
+    desc = llm.make_kv_desc(heads, 64, 16, dtype=KIND[kind], cache_dtype=KIND[cache], read_dtype=KIND[read])
+    x, slots = base.normal(base.gen(1), 40, heads, 64, kind=kind).cuda(), torch.arange(-3, 37).cuda()
+    llm.cbs_kv_write(desc, x, x, slots, kc, vc, ks, vs)
+    k, v = (torch.full(x.shape, 77, dtype=base.TYPES[read], device="cuda") for _ in range(2))
+    llm.cbs_kv_read(desc, slots, kc, vc, k, v, ks, vs)
+    assert (k == 0).all() and (v == 0).all()
+    kc, vc, ks, vs = base.kv_buffers(1, heads, 64, 16, cache)
+    none = torch.empty(heads, 0, 64, dtype=base.TYPES[read], device="cuda").transpose(0, 1)
+    llm.cbs_kv_read(desc, slots[:0], kc, vc, none, none, ks, vs)

@@ -117,6 +117,14 @@ def test_kv_read_into_overlapping_vectors(llm, args):
     assert status(llm, "cbs_kv_read", "kv", KV, {**KV_ARGS, **args}) == llm.CBS_EINVAL
 
 
+@pytest.mark.parametrize("fn", ["cbs_kv_write", "cbs_kv_read"])
+@pytest.mark.parametrize("args", [
+    dict(k_token_stride=64, k_head_stride=64), dict(v_token_stride=0, v_head_stride=0), dict(pages=0, k_cache=None, v_cache=None, k_scale=None, v_scale=None)])
+def test_kv_of_nothing(llm, fn, args):
+    """No tokens, whatever their strides (those of a transposed empty tensor among them), and a cache of no pages."""
+    assert status(llm, fn, "kv", KV, {**KV_ARGS, "tokens": 0, "k": None, "v": None, "slots": None, **args}) == llm.CBS_OK
+
+
 @pytest.mark.parametrize("desc,want", [
     (dict(heads=3), "EINVAL"), (dict(kv_heads=0), "EINVAL"), (dict(heads=0), "EINVAL"), (dict(head_dim=40), "EUNSUPPORTED"), (dict(page_size=24), "EUNSUPPORTED"),
     (dict(dtype=1), "EINVAL"), (dict(cache_dtype=3), "EUNSUPPORTED"), (dict(cache_dtype=0, dtype=0), "EUNSUPPORTED"), (dict(causal=2), "EINVAL"),
