@@ -53,6 +53,12 @@ cbs_status check_rows(const char *where, const char *what, int64_t rows, int64_t
   return CBS_OK;
 }
 
+// Of rows that are read and rows that are written, bytes apart: where they begin in one place, row lies on row.
+cbs_status check_same_rows(const char *where, const char *what, int64_t rows, const void *in, int64_t in_pitch, const void *out, int64_t out_pitch) {
+  if (!in || in != out || rows < 2 || in_pitch == out_pitch) return CBS_OK;
+  return refuse(CBS_EINVAL, where, "%s begins at an input whose rows are %lld bytes apart, its own %lld", what, (long long)in_pitch, (long long)out_pitch);
+}
+
 // Vectors of `heads` heads of `tokens` tokens.
 cbs_status check_heads(const char *where, const char *what, int64_t tokens, int64_t token_stride, int heads, int64_t head_stride,
                        int dim, bool out) {
@@ -259,6 +265,12 @@ cbs_status cbs_rms_norm(const cbs_rms_desc *d, const cbs_rms_args *a, void *stre
   if (st == CBS_OK && a->residual) st = check_rows(where, "residual", a->rows, a->residual_stride, d->dim, false);
   if (st == CBS_OK) st = check_rows(where, "out", a->rows, a->out_stride, d->dim, true);
   if (st == CBS_OK && a->residual_out) st = check_rows(where, "residual_out", a->rows, a->residual_out_stride, d->dim, true);
+  const int64_t size = d->dtype == CBS_F32 ? 4 : 2, out_pitch = a->out_stride * (d->out_dtype == CBS_I8 ? 1 : size);
+  if (st == CBS_OK && a->rows > 0 && a->out == a->residual_out) st = refuse(CBS_EINVAL, where, "out is residual_out");
+  if (st == CBS_OK) st = check_same_rows(where, "out", a->rows, a->x, a->x_stride * size, a->out, out_pitch);
+  if (st == CBS_OK) st = check_same_rows(where, "out", a->rows, a->residual, a->residual_stride * size, a->out, out_pitch);
+  if (st == CBS_OK) st = check_same_rows(where, "residual_out", a->rows, a->x, a->x_stride * size, a->residual_out, a->residual_out_stride * size);
+  if (st == CBS_OK) st = check_same_rows(where, "residual_out", a->rows, a->residual, a->residual_stride * size, a->residual_out, a->residual_out_stride * size);
   if (st != CBS_OK || a->rows == 0) return st;
   return launched(launch_rms_norm(*d, *a, (hipStream_t)stream), where);
 }

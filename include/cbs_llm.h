@@ -72,11 +72,12 @@ typedef struct cbs_rms_args {
     const void *x;        /* [rows][dim] */
     const void *residual; /* [rows][dim], NULL: none */
     const void *weight;   /* [dim] */
-    void *out;            /* [rows][dim]; may be x */
-    void *residual_out;   /* [rows][dim]: the sum; may be x or residual; NULL: not kept */
+    void *out;            /* [rows][dim] */
+    void *residual_out;   /* [rows][dim]: the sum; NULL: not kept */
     float *out_scale;     /* [rows], out_dtype CBS_I8 only */
     int64_t rows;
     int64_t x_stride, residual_stride, out_stride, residual_out_stride; /* between rows; inputs >= 0, outputs >= dim */
+    /* Either output may be x or residual, with as many bytes between its rows, and overlaps nothing else. */
 } cbs_rms_args;
 
 /* Errors: CBS_EINVAL (NULL or contradictory argument), CBS_EUNSUPPORTED (a size or type that is not offered), CBS_ELAUNCH. */

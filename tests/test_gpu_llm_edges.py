@@ -353,3 +353,21 @@ def test_kv_of_an_empty_cache(kind, cache, read, heads):
     kc, vc, ks, vs = base.kv_buffers(1, heads, 64, 16, cache)
     none = torch.empty(heads, 0, 64, dtype=base.TYPES[read], device="cuda").transpose(0, 1)
     llm.cbs_kv_read(desc, slots[:0], kc, vc, none, none, ks, vs)
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 512), (7, 512), (40, 1000)])
+def test_norm_int8_rows_into_their_input(rows, dim):
+    """Codes into the bytes of the row that they come from; the sum into the residual."""
+    g = base.gen(rows)
+    x, r = (base.normal(g, rows, dim, kind="bf16").cuda() for _ in range(2))
+    w = torch.ones(dim, dtype=torch.bfloat16, device="cuda")
+    desc = llm.make_rms_desc(dim, out_dtype=llm.CBS_I8)
+    step = [torch.empty(rows, device="cuda") for _ in range(2)]
+    want, h = torch.empty(rows, dim, dtype=torch.int8, device="cuda"), torch.empty_like(x)
+    llm.cbs_rms_norm(desc, x, w, want, residual=r, residual_out=h, out_scale=step[0])
+    codes = x.view(torch.int8)[:, :dim]
+    llm.cbs_rms_norm(desc, x, w, codes, residual=r, residual_out=r, out_scale=step[1])
+    assert torch.equal(codes, want) and torch.equal(*step) and torch.equal(r, h)
+    if rows > 1:
+        with pytest.raises(llm.CbsError, match="begins at"):
+            llm.cbs_rms_norm(desc, r, w, r.view(torch.int8).flatten()[: rows * dim].view(rows, dim), out_scale=step[0])

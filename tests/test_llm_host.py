@@ -87,6 +87,24 @@ def test_rms_norm_refusals(llm, desc, args, want):
     assert status(llm, "cbs_rms_norm", "rms", {**RMS, **desc}, {**RMS_ARGS, **args}) == getattr(llm, "CBS_" + want)
 
 
+B = A + (1 << 19)
+
+
+@pytest.mark.parametrize("desc,args", [
+    (dict(out_dtype=1), dict(out=A, out_scale=B)),                                          # int8 rows closer together than x's
+    ({}, dict(out=A, out_stride=80)),
+    ({}, dict(x_stride=0)),                                                                 # one row for all, and written
+    ({}, dict(x=B, residual=A, residual_stride=72)),
+    ({}, dict(out=B, residual=B + 1024, residual_stride=64, residual_out=A, residual_out_stride=65)),
+    ({}, dict(x=B, out=B, residual=A, residual_stride=0, residual_out=A, residual_out_stride=64)),
+    ({}, dict(x=B, residual=B, residual_stride=64, residual_out=A, residual_out_stride=64)),  # both outputs
+])
+def test_rms_norm_into_its_input(llm, desc, args):
+    """An output where an input lies, whose rows lie elsewhere: a row would be written before others are read."""
+    assert status(llm, "cbs_rms_norm", "rms", {**RMS, **desc}, {**RMS_ARGS, **args}) == llm.CBS_EINVAL
+    assert "begins at" in llm.lib.cbs_last_error().decode() or "out is residual_out" in llm.lib.cbs_last_error().decode()
+
+
 @pytest.mark.parametrize("desc,args,want", [
     (dict(k=0), {}, "EINVAL"), (dict(n=-1), {}, "EINVAL"), (dict(k=(1 << 24) + 1), {}, "EUNSUPPORTED"), (dict(group=0), {}, "EINVAL"),
     (dict(group=16), {}, "EUNSUPPORTED"), (dict(group=96), {}, "EUNSUPPORTED"), (dict(group=192), {}, "EUNSUPPORTED"), (dict(dtype=2), {}, "EINVAL"),
