@@ -87,9 +87,10 @@ class Decoder:
         self.out = torch.empty(max_rows, c.hidden, dtype=torch.bfloat16, device=dev)
 
     def slots(self, seq, place):
-        """Cache slots of sequences' places (tensors of one shape on the GPU)."""
-        page = self.cfg.page
-        return self.table[seq, place // page].long() * page + place % page
+        """Cache slots of sequences' places (tensors of one shape on the GPU); past max_len's pages -1, which is not written."""
+        page, columns = self.cfg.page, self.table.shape[1]
+        column = place // page
+        return torch.where(column < columns, self.table[seq, column.clamp(max=columns - 1)].long() * page + place % page, -1)
 
     def forward(self, x, q_start, kv_len, table, slots, max_new, max_kv):
         """The blocks over rows x of new tokens, whose keys and values go to `slots`; returns a buffer's rows."""
@@ -118,6 +119,8 @@ class Decoder:
     def prompt(self, seq, x, chunk=512):
         """A sequence's rows x in chunks after what is cached of it; returns the last row."""
         have, last = int(self.kv_len[seq]), None
+        if have + x.shape[0] > self.table.shape[1] * self.cfg.page:
+            raise ValueError("%d tokens after %d: there is room for %d" % (x.shape[0], have, self.table.shape[1] * self.cfg.page))
         for at in range(0, x.shape[0], chunk):
             part = x[at : at + chunk]
             n, first = part.shape[0], have + at
@@ -129,10 +132,10 @@ class Decoder:
 
     def single(self, rows):
         """One new token in every sequence: rows [max_seqs][hidden] become the outputs.  Lengths and slots are computed on the
-        GPU, so that the call can be captured and replayed."""
+        GPU, so that the call can be captured and replayed.  A sequence that has no room left keeps what is cached, and its lengths."""
         seq = torch.arange(self.max_seqs, device=rows.device)
         slots = self.slots(seq, self.kv_len.long())
-        self.kv_len += 1
+        self.kv_len.add_(1).clamp_(max=self.table.shape[1] * self.cfg.page)
         starts = torch.arange(self.max_seqs + 1, dtype=torch.int32, device=rows.device)
         rows.copy_(self.forward(rows, starts, self.kv_len, self.table, slots, 1, self.table.shape[1] * self.cfg.page))
 

@@ -371,3 +371,29 @@ def test_norm_int8_rows_into_their_input(rows, dim):
     if rows > 1:
         with pytest.raises(llm.CbsError, match="begins at"):
             llm.cbs_rms_norm(desc, r, w, r.view(torch.int8).flatten()[: rows * dim].view(rows, dim), out_scale=step[0])
+
+
+# ---------------------------------------------------------------- the example's decoder
+
+
+def test_decoder_past_its_pages():
+    """Single tokens go on where a sequence has no room: what is cached stays, the other's goes on as it would."""
+    from convolution_implicit_gemm_02_amd import decoder_step as ds
+    small = dict(hidden=256, heads=4, kv_heads=2, head_dim=64, ffn=640, layers=2, group=64, page=16)
+    x = torch.randn(2, 30, 256, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").bfloat16()
+    got = []
+    for long in (29, 20):
+        decoder = ds.Decoder(ds.Config(**small), 2, 32, 32, seed=5)
+        assert decoder.table.shape == (2, 2)
+        rows = torch.stack([decoder.prompt(0, x[0, :long]), decoder.prompt(1, x[1, :10])])
+        for step in range(8):
+            decoder.single(rows)
+            if long + step + 1 == 32:
+                full = [t.clone() for layer in range(2) for t in decoder.cached(layer, 0)]
+        got.append((rows[1].clone(), [t for layer in range(2) for t in decoder.cached(layer, 1)]))
+        assert decoder.kv_len.tolist() == [min(long + 8, 32), 18] and rows.isfinite().all()
+        if long == 29:
+            assert all(torch.equal(a, b) for a, b in zip(full, [t for layer in range(2) for t in decoder.cached(layer, 0)]))
+    assert torch.equal(got[0][0], got[1][0]) and all(torch.equal(a, b) for a, b in zip(got[0][1], got[1][1]))
+    with pytest.raises(ValueError, match="room"):
+        decoder.prompt(1, x[1, :15])
