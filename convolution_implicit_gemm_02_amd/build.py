@@ -220,10 +220,13 @@ def check_mfma_guards(hipcc: str) -> None:
 
 
 def bind_command(out: str):
-    """Compile and link the extension module (host code alone) against the torch that runs it."""
+    """Compile and link the extension module (host code alone) against the torch that runs it; None where there is no torch."""
     import sysconfig
-    import torch
-    from torch.utils import cpp_extension
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError:
+        return None
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     return [_hipcc(), "-shared", "-fPIC", "-O2", "-std=c++17", "-w", "--offload-host-only", "-DUSE_ROCM",
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI] + \
@@ -232,7 +235,8 @@ def bind_command(out: str):
 
 
 def build(verbose: bool = True) -> str:
-    """Compile every source and link libcbs.so and the extension module.  Always recompiles."""
+    """Compile every source and link libcbs.so, which needs hipcc alone, and where torch is there the extension module.  Always
+    recompiles."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     hipcc = _hipcc()
     check_mfma_guards(hipcc)
@@ -261,9 +265,14 @@ def build(verbose: bool = True) -> str:
                 + COMMON + DEVICE_FLAGS)
     objs.append(h_obj)
     bind_tmp = BIND_PATH + ".tmp%d" % os.getpid()
-    cmds.insert(0, bind_command(bind_tmp))  # the longest: first
+    bind = bind_command(bind_tmp)
+    if bind:
+        cmds.insert(0, bind)  # the longest: first
+    else:
+        print("no torch: the library for C programs alone, without the Python extension module", flush=True)
     _parallel(cmds)
-    os.replace(bind_tmp, BIND_PATH)
+    if bind:
+        os.replace(bind_tmp, BIND_PATH)
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     _run([hipcc, "-shared", "-o", tmp] + objs + ["--offload-arch=" + ARCH, "-fPIC"])
     os.replace(tmp, LIB_PATH)
