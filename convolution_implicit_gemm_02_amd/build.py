@@ -219,6 +219,68 @@ def check_mfma_guards(hipcc: str) -> None:
         raise RuntimeError("kernel argument read after the main loop, or FLAT access, in: %s" % ", ".join(late))
 
 
+def miscounted_waits(text: str, ring: str = r"^(_ZN3cbs\S*14w4_ring_kernelI\w+):", chunk: str = r"^(_ZN3cbs\S*17attn_chunk_kernelI\w+):"):
+    """Kernels of a device assembly that wait for loads by a number of later ones which are not there: a wait until N loads are
+    outstanding is one for the loads to LDS only where N at least were issued behind them.  Returns (flagged names, number of
+    kernels looked at).
+
+    ring: a wait before a barrier has its N loads to registers (those of a block of codes) in its own basic block, so on every
+    way to it; N is that of the kernel's template arguments.  chunk: all loads that are counted go to LDS, a tile's in each turn of the
+    loop and AHEAD tiles' before it; the first wait is for all but one of those tiles, the next for one more."""
+    import re
+    bad, found = [], 0
+    wait = re.compile(r"s_waitcnt vmcnt\((\d+)\)")
+    for pattern in (ring, chunk):
+        for name in re.findall(pattern, text, re.M):
+            i = text.index(name + ":")
+            body = [line.strip() for line in text[i:text.index(".Lfunc_end", i)].split("\n")]
+            body = [line for line in body if line and not line.startswith(";")]
+            found += 1
+            if pattern == ring:
+                nb, steps = (int(v) for v in re.search(r"kernelILi\d+ELi(\d+)ELi(\d+)E", name).groups())
+                counted = []
+                for k, line in enumerate(body[:-1]):
+                    m = wait.match(line)
+                    if not m or int(m.group(1)) == 0 or body[k + 1] != "s_barrier":
+                        continue
+                    loads = 0
+                    for before in reversed(body[:k]):
+                        if before.startswith((".L", "s_cbranch", "s_branch", "global_load_lds")):
+                            break
+                        loads += before.startswith("global_load")
+                    counted.append((int(m.group(1)), loads))
+                want = nb * (1 + 2 * (4 // steps))
+                if counted != [(want, want)] * 2:
+                    bad.append(name)
+            else:
+                loads = sum(line.startswith("global_load_lds") for line in body)
+                first = next((k for k, line in enumerate(body) if line.startswith("global_load_lds")), 0)
+                # the waits written by hand wait for LDS operations, too
+                waits = [int(wait.match(line).group(1)) for line in body[first:] if wait.match(line) and line.endswith("lgkmcnt(0)")]
+                waits = [n for n in waits if n > 1]
+                tile = waits[0] - next((n for n in waits if n != waits[0]), 0) if waits else 0
+                if not waits or tile < 1 or waits[0] % tile or loads != waits[0] + 2 * tile:
+                    bad.append(name)
+    return bad, found
+
+
+# sources whose kernels wait by counts: assembly's name, source, defines, kernels
+COUNTED = [("llm_w4_%d" % n, "llm_w4.hip", ["-DCBS_W4_X=%d" % n], 44) for n in range(3)] + \
+          [("llm_attn_%d" % n, "llm_attn.hip", ["-DCBS_ATTN_PAIR=%d" % n], 4) for n in range(4)]
+
+
+def check_wait_counts(hipcc: str) -> None:
+    """Fail the build if a decoder-step kernel's loads are not as many as its waits count on."""
+    _parallel([[hipcc, "--cuda-device-only", "-S", os.path.join(CSRC, src), "-o", os.path.join(BUILD_DIR, name + ".s"), "-O3"] + defs
+               + COMMON + DEVICE_FLAGS for name, src, defs, _ in COUNTED])
+    for name, _, _, kernels in COUNTED:
+        bad, found = miscounted_waits(open(os.path.join(BUILD_DIR, name + ".s")).read())
+        if found != kernels:
+            raise RuntimeError("%s: %d kernels that wait by counts, expected %d" % (name, found, kernels))
+        if bad:
+            raise RuntimeError("a wait's count is not that of the loads behind it in: %s" % ", ".join(bad))
+
+
 def bind_command(out: str):
     """Compile and link the extension module (host code alone) against the torch that runs it; None where there is no torch."""
     import sysconfig
@@ -240,6 +302,7 @@ def build(verbose: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     hipcc = _hipcc()
     check_mfma_guards(hipcc)
+    check_wait_counts(hipcc)
     objs, cmds = [], []
     k_obj = os.path.join(BUILD_DIR, "cbs_kernels.o")
     cmds.append([hipcc, "-c", os.path.join(CSRC, "cbs_kernels.hip"), "-o", k_obj, "-O3"] + COMMON + DEVICE_FLAGS)
