@@ -19,7 +19,8 @@
  *   or as it is (cache_dtype CBS_F16 or CBS_BF16), and read back as T(fp32(q_i * s)) or as it is.
  * Attention: new token i (0 <= i < count) of a sequence that has length tokens, its new ones included, is at
  *   place = length - count + i, and sees key j if 0 <= j < length, causal: j <= place, window w > 0: j > place - w.
- *   out_i = sum_j p_j v_j / sum_j p_j over the keys that it sees, p_j = exp(scale * q_i . k_j - max); 0 where it sees none.
+ *   out_i = sum_j p_j v_j / sum_j p_j over the keys that it sees, p_j = exp(scale * q_i . k_j - max); 0 where it sees none, or
+ *   none but of a score of -infinity.
  *   Head h reads the cache's head h / (heads / kv_heads).  What the cache holds where no key is seen, NaN and infinities
  *   among it, does not reach the output.  With 16-bit queries the weights p_j are rounded to 16 bits before they meet the
  *   values.  One that its type does not hold is zero (over a float16 cache below 2^-32 of the row's largest, else below that of

@@ -166,6 +166,64 @@ def test_attn_most_rows_there_can_be():
         assert (part == want).all()
 
 
+
+@pytest.mark.parametrize("kind,cache", base.PAIRS)
+@pytest.mark.parametrize("scale", [-0.125, 0.0, -0.0, 3.0, 1e-30])
+@pytest.mark.parametrize("new,kv,window", [([1, 40], [70, 300], 0), ([140, 9], [300, 77], 0), ([140, 9], [300, 77], 45)])
+def test_attn_scales(kind, cache, scale, new, kv, window):
+    """Negative scales turn the order of the keys; one of zero has all keys' mean."""
+    check_made(deep(base.make_attn(new, kv, 4, 2, 64, 16, kind, cache, q_by=0.5)), 4, 2, 64, kind, cache, window=window, scale=scale)
+
+
+@pytest.mark.parametrize("kind,cache", base.PAIRS)
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("new", [[1, 1], [40, 3], [140, 9]])
+def test_attn_nonfinite_queries(kind, cache, bad, new):
+    """A query that holds a NaN, or an infinity that some key's feature lifts above all or meets as zero, has NaN; all others stay."""
+    made = list(deep(base.make_attn(new, [300, 77], 4, 2, 64, 16, kind, cache)))
+    clean = base.run_attn(made, 4, 2, 64, 16, kind, cache)
+    made[0] = made[0].clone()
+    rows = [(0, 1), (sum(new) - 1, 3), (sum(new) // 2, 0)]
+    for t, h in rows:
+        made[0][t, h, 5] = bad
+    out = base.run_attn(made, 4, 2, 64, 16, kind, cache)
+    hit = torch.zeros(out.shape[:2], dtype=torch.bool)
+    for t, h in rows:
+        hit[t, h] = True
+    assert torch.isnan(out[hit]).all() and torch.equal(out[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("kind,cache", [("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("new", [1, 40, 140])
+def test_attn_scores_of_minus_infinity(kind, cache, new):
+    """Keys of minus infinity weigh nothing, with others beside them and without."""
+    made = list(deep(base.make_attn([new], [300], 2, 1, 64, 16, kind, cache)))
+    q, q_start, kv_len, table, k, v, _, _ = made
+    q[..., 3] = q[..., 3].abs() + 1
+    lost = [j for j in range(300) if j % 3]
+    beside = [t.clone() for t in made[4:6]]
+    for j in lost:
+        beside[0][int(table[0, j // 16]), :, j % 16, 3] = -math.inf
+    out = base.run_attn((q, q_start, kv_len, table, *beside, None, None), 2, 1, 64, 16, kind, cache)
+    _, _, tops = ref.attention(q, q_start, kv_len, table, k, v, 64 ** -0.5)  # of finite scores
+    want, mags, _ = ref.attention(q, q_start, kv_len, table, *beside, 64 ** -0.5)
+    base.close(out, want, base.attn_bound(want, mags, tops, kind, 64, 300), "beside others")
+    for j in range(300):
+        beside[0][int(table[0, j // 16]), :, j % 16, 3] = -math.inf
+    assert (base.run_attn((q, q_start, kv_len, table, *beside, None, None), 2, 1, 64, 16, kind, cache) == 0).all()
+
+
+@pytest.mark.parametrize("kind,cache", base.PAIRS)
+@pytest.mark.parametrize("max_new", [None, 200, 1, 7])
+def test_attn_chunk_beside_single_tokens(kind, cache, max_new):
+    """One call of a chunk and of single tokens, on each of the kernels."""
+    new, kv = [200, 1, 1, 7, 1, 0], [700, 1, 900, 7, 2000, 40]
+    made = deep(base.make_attn(new, kv, 4, 1, 64, 16, kind, cache))
+    out = base.run_attn(made, 4, 1, 64, 16, kind, cache, max_new=max_new)
+    want, mags, tops = ref.attention(made[0], made[1], made[2], made[3], made[4], made[5], 64 ** -0.5, k_scale=made[6], v_scale=made[7])
+    base.close(out, want, base.attn_bound(want, mags, tops, kind, 64, 2000), "mixed")
+
+
 # ---------------------------------------------------------------- more than one launch takes
 
 
