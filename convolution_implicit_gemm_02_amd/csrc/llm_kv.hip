@@ -103,7 +103,8 @@ __device__ __forceinline__ Slots slots_of(const KvParams &p, int64_t tile, int l
   for (int j = 0; j < 4; j++) s.quads |= (((chain >> (4 * j)) & 14) == 14) << j;
   return s;
 }
-// Byte of the first feature of token t's values in the cache, wave-uniform; -1 where it has none.
+// Byte of the first feature of token t's values in the cache, wave-uniform; -1 where it has none.  Only where all lanes are on: one
+// that is off need not hold anything.
 template <int B>
 __device__ __forceinline__ int64_t values_at(const KvParams &p, const Slots &s, int t, int h) {
   const int page = __builtin_amdgcn_readlane(s.page, t), place = __builtin_amdgcn_readlane(s.place, t);
@@ -167,7 +168,9 @@ __device__ __forceinline__ void values_out(const KvParams &p, const Slots &s, co
   const int dim = p.d.head_dim, pitch = pitch_of<I8>(dim);
   const uint32_t step = (uint32_t)p.d.page_size * B;  // from a feature to the next; a page's head is below 2^20 bytes
   char *cache = (char *)p.a.v_cache;
-  for (int f0 = lane * E; f0 < dim; f0 += 64 * E) {
+  for (int first = 0; first < dim; first += 64 * E) {
+    const bool mine = first + lane * E < dim;  // a lane without features has the last ones, for nothing
+    const int f0 = min(first + lane * E, dim - E);
     uint32_t in[kTile], out[E][PER];
 #pragma unroll
     for (int t = 0; t < kTile; t++) in[t] = *(const uint32_t *)(lds + t * pitch + f0 * B);
@@ -175,16 +178,20 @@ __device__ __forceinline__ void values_out(const KvParams &p, const Slots &s, co
     const uint32_t off = (uint32_t)f0 * step;
     if (s.whole) {
       char *to = cache + values_at<B>(p, s, 0, h);
+      if (mine) {
 #pragma unroll
-      for (int i = 0; i < E; i++) __builtin_memcpy(to + (off + i * step), out[i], kTile * B);
+        for (int i = 0; i < E; i++) __builtin_memcpy(to + (off + i * step), out[i], kTile * B);
+      }
       continue;
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
       if (s.quads >> j & 1) {
         char *to = cache + values_at<B>(p, s, 4 * j, h);
+        if (mine) {
 #pragma unroll
-        for (int i = 0; i < E; i++) __builtin_memcpy(to + (off + i * step), &out[i][j * B], 4 * B);
+          for (int i = 0; i < E; i++) __builtin_memcpy(to + (off + i * step), &out[i][j * B], 4 * B);
+        }
         continue;
       }
 #pragma unroll
@@ -192,11 +199,13 @@ __device__ __forceinline__ void values_out(const KvParams &p, const Slots &s, co
         const int64_t at = values_at<B>(p, s, t, h);
         if (at < 0) continue;
         char *to = cache + at;
+        if (mine) {
 #pragma unroll
-        for (int i = 0; i < E; i++) {
-          const uint32_t v = out[i][t * B / 4] >> (8 * B * (t % E));
-          if constexpr (I8) *(uint8_t *)(to + (off + i * step)) = (uint8_t)v;
-          else *(uint16_t *)(to + (off + i * step)) = (uint16_t)v;
+          for (int i = 0; i < E; i++) {
+            const uint32_t v = out[i][t * B / 4] >> (8 * B * (t % E));
+            if constexpr (I8) *(uint8_t *)(to + (off + i * step)) = (uint8_t)v;
+            else *(uint16_t *)(to + (off + i * step)) = (uint16_t)v;
+          }
         }
       }
     }
@@ -209,40 +218,47 @@ __device__ __forceinline__ void values_in(const KvParams &p, const Slots &s, uns
   const int dim = p.d.head_dim, pitch = pitch_of<I8>(dim);
   const uint32_t step = (uint32_t)p.d.page_size * B;
   const char *cache = (const char *)p.a.v_cache;
-  for (int f0 = lane * E; f0 < dim; f0 += 64 * E) {
+  for (int first = 0; first < dim; first += 64 * E) {
+    const bool mine = first + lane * E < dim;  // as above
+    const int f0 = min(first + lane * E, dim - E);
     uint32_t in[E][PER], out[kTile];
     const uint32_t off = (uint32_t)f0 * step;
     if (s.whole) {
       const char *from = cache + values_at<B>(p, s, 0, h);
+      if (mine) {
 #pragma unroll
-      for (int i = 0; i < E; i++) __builtin_memcpy(in[i], from + (off + i * step), kTile * B);
-    } else {
+        for (int i = 0; i < E; i++) __builtin_memcpy(in[i], from + (off + i * step), kTile * B);
+        to_tokens<E>(in, out);
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        if (s.quads >> j & 1) {
-          const char *from = cache + values_at<B>(p, s, 4 * j, h);
+        for (int t = 0; t < kTile; t++) *(uint32_t *)(lds + t * pitch + f0 * B) = out[t];
+      }
+      continue;
+    }
 #pragma unroll
-          for (int i = 0; i < E; i++) __builtin_memcpy(&in[i][j * B], from + (off + i * step), 4 * B);
-          continue;
-        }
-        uint32_t one[4][E];  // all read, of the cache's first page where a token has none: one wait
+    for (int j = 0; j < 4; j++) {
+      if (s.quads >> j & 1) {
+        const char *from = cache + values_at<B>(p, s, 4 * j, h);
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-          const int64_t at = values_at<B>(p, s, 4 * j + k, h);
-          const char *from = cache + max(at, (int64_t)0);
+        for (int i = 0; i < E; i++) __builtin_memcpy(&in[i][j * B], from + (off + i * step), 4 * B);
+        continue;
+      }
+      uint32_t one[4][E];  // all read, of the cache's first page where a token has none: one wait
 #pragma unroll
-          for (int i = 0; i < E; i++) {
-            if (p.a.pages == 0) one[k][i] = 0;
-            else if constexpr (I8) one[k][i] = *(const uint8_t *)(from + (off + i * step));
-            else one[k][i] = *(const uint16_t *)(from + (off + i * step));
-            if (at < 0) one[k][i] = 0;
-          }
-        }
+      for (int k = 0; k < 4; k++) {
+        const int64_t at = values_at<B>(p, s, 4 * j + k, h);
+        const char *from = cache + max(at, (int64_t)0);
 #pragma unroll
         for (int i = 0; i < E; i++) {
-          if constexpr (I8) in[i][j] = one[0][i] | one[1][i] << 8 | one[2][i] << 16 | one[3][i] << 24;
-          else in[i][2 * j] = one[0][i] | one[1][i] << 16, in[i][2 * j + 1] = one[2][i] | one[3][i] << 16;
+          if (p.a.pages == 0) one[k][i] = 0;
+          else if constexpr (I8) one[k][i] = *(const uint8_t *)(from + (off + i * step));
+          else one[k][i] = *(const uint16_t *)(from + (off + i * step));
+          if (at < 0) one[k][i] = 0;
         }
+      }
+#pragma unroll
+      for (int i = 0; i < E; i++) {
+        if constexpr (I8) in[i][j] = one[0][i] | one[1][i] << 8 | one[2][i] << 16 | one[3][i] << 24;
+        else in[i][2 * j] = one[0][i] | one[1][i] << 16, in[i][2 * j + 1] = one[2][i] | one[3][i] << 16;
       }
     }
     to_tokens<E>(in, out);
