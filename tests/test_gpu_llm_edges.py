@@ -81,7 +81,7 @@ def check_made(made, heads, kv_heads, dim, kind, cache, causal=True, window=0, s
 
 @pytest.mark.parametrize("kind,cache", base.PAIRS)
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 5, 2**31 - 200])
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 200])
 @pytest.mark.parametrize("new,kv", [([10, 6, 1], [4, 6, 0]), ([300, 150], [41, 149])])
 def test_attn_window_of_all_there_can_be(kind, cache, causal, window, new, kv):
     """More new tokens than keys, and a window near 2^31: places before the first key, and the rows beside them, keep theirs."""
@@ -89,13 +89,12 @@ def test_attn_window_of_all_there_can_be(kind, cache, causal, window, new, kv):
     check_made(made if len(new) == 3 else deep(made), 4, 2, 64, kind, cache, causal, window)
 
 
-@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-@pytest.mark.parametrize("which", ["key", "value", "both"])
+@pytest.mark.parametrize("bad,which", [(math.nan, "key"), (math.nan, "value"), (math.inf, "value"), (-math.inf, "both")])
 @pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("key", [70, 200, 300])
+@pytest.mark.parametrize("key", [200, 300])
 @pytest.mark.parametrize("new", [1, 40, 130])
 def test_attn_nonfinite_steps_seen(bad, which, kind, key, new):
-    """A step that is infinite or NaN, in a tile that all rows see whole (70, 200) and in one that some of them see in part (300):
+    """A step that is infinite or NaN, in a tile that all rows see whole (200) and in one that some of them see in part (300):
     rows that do not see it stay as they are, and those that do have what the formula says of a NaN, and of an infinite step of values."""
     heads, dim, page, kv = 4, 64, 16, 310
     made = deep(base.make_attn([new], [kv], heads, 2, dim, page, kind, "i8", q_by=0.3))
@@ -168,7 +167,7 @@ def test_attn_most_rows_there_can_be():
 
 
 @pytest.mark.parametrize("kind,cache", base.PAIRS)
-@pytest.mark.parametrize("scale", [-0.125, 0.0, -0.0, 3.0, 1e-30])
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 3.0])
 @pytest.mark.parametrize("new,kv,window", [([1, 40], [70, 300], 0), ([140, 9], [300, 77], 0), ([140, 9], [300, 77], 45)])
 def test_attn_scales(kind, cache, scale, new, kv, window):
     """Negative scales turn the order of the keys; one of zero has all keys' mean."""
@@ -176,7 +175,7 @@ def test_attn_scales(kind, cache, scale, new, kv, window):
 
 
 @pytest.mark.parametrize("kind,cache", base.PAIRS)
-@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
 @pytest.mark.parametrize("new", [[1, 1], [40, 3], [140, 9]])
 def test_attn_nonfinite_queries(kind, cache, bad, new):
     """A query that holds a NaN, or an infinity that some key's feature lifts above all or meets as zero, has NaN; all others stay."""
