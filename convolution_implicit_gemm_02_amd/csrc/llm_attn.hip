@@ -522,8 +522,8 @@ struct ChunkLds {
 // widened from there, once for all waves.
 //
 // Tile t + 1's scores are taken and tile t - 1's values added on the matrix cores while tile t's scores become weights, a few
-// instructions of each in turn.  Two sequences of 512 new tokens, 32 heads over 8 of bfloat16 and 8192 tokens: 162 us with the
-// join, 750 TFLOP/s, where a large matrix product reaches 1109; the vector instructions of the weights bound it.
+// instructions of each in turn.  Two sequences of 512 new tokens, 32 heads over 8 of bfloat16 and 8192 tokens: 160 us with the
+// join, 760 TFLOP/s, where a large matrix product reaches 1109; the vector instructions of the weights bound it.
 template <int QK, int CK, int DS, int RB>
 __global__ __launch_bounds__(kAttnChunkThreads, 2) void attn_chunk_kernel(const AttnParams p) {
   constexpr bool I8 = CK == CBS_I8, SF16 = QK == CBS_F16, PF16 = CK == CBS_F16;

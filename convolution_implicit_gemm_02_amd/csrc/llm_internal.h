@@ -99,8 +99,9 @@ __device__ __forceinline__ float code_step(float top) {
 __device__ __forceinline__ int code_of(float v, float step) {
   return (int)fminf(fmaxf(rintf(__fdiv_rn(v, step)), -127.0f), 127.0f);
 }
-// N of them, a multiple of four.  The quotient as a product with the step's reciprocal, corrected by its remainder: with a
-// correctly rounded reciprocal that is the correctly rounded quotient, in a third of a division's instructions.  The remainder
+// N of them, a multiple of four.  The quotient as a product with the step's reciprocal, corrected by its remainder (Markstein,
+// IBM J. Res. Dev. 34, 1990): with a correctly rounded reciprocal that is the correctly rounded quotient, in a third of a division's
+// instructions.  The remainder
 // needs room below: steps under 2^-100 go the long way.  1.5 times 2^23 added rounds to a whole number, whose two's complement
 // the low bits then are.
 template <int N>

@@ -69,13 +69,14 @@ __global__ __launch_bounds__(256) void kv_kernel(const KvParams p) {
 // ---- many tokens: one wave per 16 tokens of one head.  A token's vector lies on four lanes, lane l's being token l / 4: pieces
 // of 16 features, 4 n + l % 4 for n = 0, 1, ...  The value cache has a feature's tokens side by side: vectors turn in LDS, so
 // that 16 tokens (or four) whose slots follow one another in a page are one access a feature.
-// The cost is the vectors' and the cache's bytes: 8191 tokens of 8 heads of 128 bfloat16 features into int8, in runs, 24 us to
-// write and 19 to read back, 2.3 TB/s (a wave per vector: 54 and 43, single bytes to the value cache).
+// The cost is the vectors' and the cache's bytes: 8191 tokens of 8 heads of 128 bfloat16 features into int8, in runs, 23 us to
+// write and 20 to read back, 2.3 TB/s (a wave per vector: 54 and 43, single bytes to the value cache).
 // Vectors (tokens times heads) from which tiles are taken, a wave a vector below; us of tiles | vectors, 8 heads:
 //   write, 4096 vectors: 128 bf16 to i8 in runs of 500 5.9 | 6.5, scattered 11.0 | 8.8; 256 bf16 9.0 | 10.8, 17.8 | 17.6
 //          8192:         6.6 | 10.0, 13.3 | 13.7;  7.9 | 18.4, 30 | 32
 //   read,  4096:         6.1 | 5.1, 10.5 | 5.2;    9.0 | 7.1, 20.9 | 13.7
 //          8192:         6.2 | 7.5, 13.5 | 9.6;    6.3 | 12.1, 25 | 27;  16384: 6.8 | 12.1, 16.7 | 18.0;  10.6 | 21.5, 45 | 53
+// The host does not see the slots: scattered ones are read at a loss from here to nearly 16384 vectors.
 constexpr int kTile = 16;
 constexpr int64_t kManyVectors = 8192;
 constexpr int64_t kMostVectors = 1 << 29;  // of a launch: a wave has 16, 2^31 threads in all

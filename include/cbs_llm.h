@@ -8,7 +8,8 @@
  * RMS norm, per row:
  *   h = T(x + residual) (h = x without one; h goes to residual_out),  y_i = h_i / sqrt(mean_j h_j^2 + eps) * w_i
  *   output of x's type: T(y);  int8: s = fp32(max_i |y_i| / 127), 1 where that is 0,  q_i = clamp(rne(fp32(y_i / s)), -127, 127).
- *   A row that holds a NaN or an infinity has the scale NaN or infinity, and codes without meaning.
+ *   A row that holds a NaN or an infinity has the scale NaN or infinity, and codes without meaning.  The sum of squares is held in
+ *   32 bits: one that leaves them (magnitudes of 2^60 and more) gives zeros, and with eps 0 one that vanishes there infinities.
  * 4-bit linear, groups g of `group` consecutive input features:
  *   y[m][n] = x_scale[m] * sum_g scales[g][n] * sum_{k in g} x[m][k] * (code[n][k] - zero[g][n])
  *   x_scale is 1 for floating rows; zero is 8 where none are given.
@@ -16,7 +17,8 @@
  *   (bfloat16 on few rows: not before the formula's own do).
  * Paged cache, of keys and values of `heads` heads:  slot = page * page_size + place;  a token's vector v of one head is kept as
  *   s = fp32(max_i |v_i| / 127), 1 where that is 0,  q_i = clamp(rne(fp32(v_i / s)), -127, 127)   (cache_dtype CBS_I8)
- *   or as it is (cache_dtype CBS_F16 or CBS_BF16), and read back as T(fp32(q_i * s)) or as it is.
+ *   or as it is (cache_dtype CBS_F16 or CBS_BF16), and read back as T(fp32(q_i * s)) or as it is.  A vector that holds a NaN or an
+ *   infinity has the step NaN or infinity, and codes without meaning.
  * Attention: new token i (0 <= i < count) of a sequence that has length tokens, its new ones included, is at
  *   place = length - count + i, and sees key j if 0 <= j < length, causal: j <= place, window w > 0: j > place - w.
  *   out_i = sum_j p_j v_j / sum_j p_j over the keys that it sees, p_j = exp(scale * q_i . k_j - max); 0 where it sees none, or
@@ -160,8 +162,8 @@ typedef struct cbs_attn_args {
     int64_t tokens, pages;
     int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride, table_stride;
     int32_t seqs, columns;
-    int32_t max_new, max_kv; /* most new tokens and most tokens of a sequence: they choose how the work is split, and where
-                                a sequence has more, the result is the same */
+    int32_t max_new, max_kv; /* most new tokens and most tokens of a sequence: they choose how the work of all of them is
+                                split, and where a sequence has more, the result is the same */
 } cbs_attn_args;
 
 /* The workspace is allocated here; a run allocates nothing.  One handle runs in one stream at a time. */
